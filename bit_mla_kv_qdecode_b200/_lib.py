@@ -13,6 +13,7 @@ import os
 from . import build as _build
 
 _c_int, _c_size, _c_void, _c_float, _c_uint = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float, ctypes.c_uint
+_c_i64 = ctypes.c_int64
 
 MLA_OK = 0
 MLA_ERR_INVALID_ARG = 1
@@ -26,6 +27,9 @@ MLA_DECODE_DEFAULT = 0
 MLA_DECODE_FORCE_SIMT = 1
 MLA_DECODE_FAST_UNCOMPENSATED = 2
 MLA_DECODE_TEST_STALL = 4  # tests only: runs the device-side timeout path
+
+MLA_ROPE_INTERLEAVED = 0
+MLA_ROPE_HALF = 1
 
 MLA_QDECODE_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -67,6 +71,20 @@ SIGNATURES = {
     "mla_qdecode_hybrid": (_c_int, [_P, _c_void, _c_void, _c_int, _c_void, _c_int, _c_void, _c_int, _c_void,
                                     _c_int, _c_void, _c_int, _c_void, _c_void, _c_int, _c_int, _c_int, _c_float,
                                     _c_void, _c_size, _c_void, _c_int, _c_void, _c_void]),
+    "mla_qcache_append_norm_rope": (_c_int, [_P, _c_void, _c_void, _c_int, _c_void, _c_void, _c_void, _c_i64, _c_void,
+                                             _c_float, _c_void, _c_i64, _c_i64, _c_int, _c_void, _c_void, _c_int,
+                                             _c_void, _c_int, _c_void, _c_int, _c_int, _c_void]),
+    "mla_qcache_read": (_c_int, [_P, _c_void, _c_void, _c_int, _c_void, _c_void, _c_int, _c_i64, _c_void, _c_i64,
+                                 _c_void, _c_i64, _c_int, _c_void]),
+    "mla_page_digest": (_c_int, [_P, _c_void, _c_void, _c_int, _c_void, _c_void, _c_int, _c_void, _c_int, _c_void]),
+    "mla_page_scores": (_c_int, [_c_void, _c_int, _c_void, _c_int, _c_void, _c_int, _c_void, _c_void, _c_int, _c_int,
+                                 _c_int, _c_float, _c_void, _c_void]),
+    "mla_select_pages": (_c_int, [_c_void, _c_int, _c_void, _c_int, _c_void, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                  _c_void, _c_void, _c_void, _c_void]),
+    "mla_qdecode_sparse_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int]),
+    "mla_qdecode_sparse": (_c_int, [_P, _c_void, _c_void, _c_int, _c_void, _c_int, _c_void, _c_void, _c_void, _c_int,
+                                    _c_int, _c_int, _c_float, _c_int, _c_int, _c_int, _c_void, _c_size, _c_void, _c_int,
+                                    _c_void, _c_uint, _c_void]),
     "mla_cache_bytes_per_request": (_c_size, [_P, ctypes.c_long, _c_int, _c_int]),
     "mla_cache_max_requests": (ctypes.c_long, [_P, ctypes.c_long, _c_int, _c_int, _c_size]),
     "mla_get_device_status": (_c_int, [ctypes.POINTER(_c_int), _c_void]),

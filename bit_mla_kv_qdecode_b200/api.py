@@ -205,6 +205,272 @@ def mla_qdecode_hybrid(desc, pool, block_table, hist_lens, max_hist_len, bf16_po
     return out, lse
 
 
+def _ints(t, name, shape, device):
+    """Address of an optional int32 tensor of the given shape on `device`."""
+    if t is None:
+        return None
+    p = _need(t, name, torch.int32, shape)
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return p
+
+
+def _on(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _empty(shape, dtype, device, stream):
+    """Uninitialised tensor for a kernel on `stream` (None: the current stream): taken from that
+    stream's memory, and not given back while the current stream may still read it."""
+    if stream is not None:
+        cur = torch.cuda.current_stream(device)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device) if int(stream) else torch.cuda.default_stream(device)
+        if stream.cuda_stream != cur.cuda_stream:
+            with torch.cuda.stream(stream):
+                t = torch.empty(shape, dtype=dtype, device=device)
+            t.record_stream(cur)
+            return t
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _call(name, device, stream, *args):
+    """Run a library call with `device` current, on `stream` or the device's current stream."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    s = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    fn = getattr(_lib.load(), name)
+    if device.index is None or torch.cuda.current_device() == device.index:
+        code = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, s)
+    if code:
+        check(name, code)
+
+
+def _pool(desc, pool):
+    """Address of a quantized pool, which must hold every page of desc."""
+    p = _need(pool, "pool", torch.uint8)
+    if pool.numel() < desc.num_pages * mla_qcache_page_bytes(desc):
+        raise ValueError("pool is smaller than desc.num_pages pages")
+    return p
+
+
+def _table(block_table, B, device):
+    p = _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must have shape ({B}, max_pages), got {tuple(block_table.shape)}")
+    _on(device, block_table=block_table)
+    return p
+
+
+def _rows(t, name, shape):
+    """(address, row stride) of a bf16 tensor [B, n, ...] whose B * n rows are evenly spaced."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    B, n = shape[0], shape[1]
+    if t.stride(-1) != 1 or (B > 1 and n > 1 and t.stride(0) != n * t.stride(1)):
+        raise ValueError(f"{name} must have unit stride in its last dimension and evenly spaced rows")
+    return t.data_ptr(), (t.stride(1) if n > 1 else t.stride(0) if B > 1 else 0)
+
+
+def _out_rows(t, name, rows, width):
+    """(address, row stride) of a bf16 output [rows, width] with unit stride in a row."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != (rows, width):
+        raise ValueError(f"{name} must have shape {(rows, width)}, got {tuple(t.shape)}")
+    if t.stride(1) != 1 or (rows > 1 and t.stride(0) < width):
+        raise ValueError(f"{name} must have unit stride in a row and rows that do not overlap")
+    return t.data_ptr(), t.stride(0) if rows > 1 else width
+
+
+_ROPE_PAIRS = {"interleaved": _lib.MLA_ROPE_INTERLEAVED, "half": _lib.MLA_ROPE_HALF}
+
+
+def mla_qcache_append_norm_rope(desc, pool, block_table, seq_lens_before, kv, norm_weight, eps, cos_sin, *,
+                                convention="interleaved", q=None, q_out=None, positions=None, new_lens=None,
+                                rows_out=None, stream=None):
+    """Append from the raw projections: RMS norm of the latent, rotation of the key and of the
+    queries, quantize and write. kv [B, n, 576] and q [B, n, H, 64] may be column ranges of wider
+    tensors; norm_weight may be None (ones); convention names the rotary pairs as in
+    fold.rotary_pairs. Returns q_out [B, n, H, 64] (None without q). See include/mla_qcache.h."""
+    if convention not in _ROPE_PAIRS:
+        raise ValueError(f"unknown rotary convention {convention!r}")
+    if not isinstance(kv, torch.Tensor) or kv.dim() != 3:
+        raise ValueError("kv must be a tensor [B, n, 576]")
+    B, n = kv.shape[0], kv.shape[1]
+    dev = kv.device
+    pkv, kv_stride = _rows(kv, "kv", (B, n, D_C + D_R))
+    H, pq, q_token, q_head, pqo = 0, None, 0, 0, None
+    if q is not None and q.dim() != 4:
+        raise ValueError("q must be a tensor [B, n, H, 64]")
+    if q is not None and q.shape[2] > 0:
+        H = q.shape[2]
+        pq, q_token = _rows(q, "q", (B, n, H, D_R))
+        q_head = q.stride(2) if H > 1 else 0
+        if q_out is None:
+            q_out = _empty((B, n, H, D_R), torch.bfloat16, dev, stream)
+        pqo = _need(q_out, "q_out", torch.bfloat16, (B, n, H, D_R))
+    elif q_out is not None:
+        if q is None:
+            raise ValueError("q_out needs q")
+        _need(q_out, "q_out", torch.bfloat16, (B, n, 0, D_R))
+    elif q is not None:
+        q_out = _empty((B, n, 0, D_R), torch.bfloat16, dev, stream)
+    pw = None if norm_weight is None else _need(norm_weight, "norm_weight", torch.bfloat16, (D_C,))
+    pcs = _need(cos_sin, "cos_sin", torch.float32)
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != D_R:
+        raise ValueError(f"cos_sin must have shape (positions, {D_R}), got {tuple(cos_sin.shape)}")
+    prows = None if rows_out is None else _need(rows_out, "rows_out", torch.bfloat16, (B, n, D_C + D_R))
+    _on(dev, pool=pool, norm_weight=norm_weight, q=q, q_out=q_out, cos_sin=cos_sin, rows_out=rows_out)
+    _call("mla_qcache_append_norm_rope", dev, stream, ctypes.byref(desc), _pool(desc, pool),
+          _table(block_table, B, dev), block_table.shape[1], _ints(seq_lens_before, "seq_lens_before", (B,), dev),
+          _ints(new_lens, "new_lens", (B,), dev), pkv, kv_stride, pw, float(eps), pq, q_token, q_head, H, pqo, pcs,
+          cos_sin.shape[0], _ints(positions, "positions", (B, n), dev), _ROPE_PAIRS[convention], prows, B, n)
+    return q_out
+
+
+def mla_qcache_read(desc, pool, block_table, start, cu_rows, max_rows, out_c=None, out_kr=None, stream=None) -> None:
+    """Read dequantized rows back: tokens start[b] + i (start None: 0) of request b into row
+    cu_rows[b] + i of out_c [rows, 512] and out_kr [rows, 64] (bf16; either may be None, and both may
+    be column ranges of one buffer). max_rows bounds the rows of one request."""
+    if not isinstance(cu_rows, torch.Tensor) or cu_rows.dim() != 1 or cu_rows.shape[0] < 1:
+        raise ValueError("cu_rows must be a tensor [B + 1]")
+    B, dev = cu_rows.shape[0] - 1, cu_rows.device
+    if out_c is None and out_kr is None:
+        raise ValueError("out_c or out_kr must be given")
+    rows = (out_c if out_c is not None else out_kr).shape[0]
+    pc, sc = (None, 0) if out_c is None else _out_rows(out_c, "out_c", rows, D_C)
+    pr, sr = (None, 0) if out_kr is None else _out_rows(out_kr, "out_kr", rows, D_R)
+    _on(dev, pool=pool, out_c=out_c, out_kr=out_kr)
+    _call("mla_qcache_read", dev, stream, ctypes.byref(desc), _pool(desc, pool), _table(block_table, B, dev),
+          block_table.shape[1], _ints(start, "start", (B,), dev), _ints(cu_rows, "cu_rows", (B + 1,), dev),
+          int(max_rows), rows, pc, sc, pr, sr, B)
+
+
+def mla_page_digest(desc, pool, block_table, seq_lens_before, n_new, digests, *, new_lens=None, stream=None) -> None:
+    """Mean keys of the pages that appending new_lens[b] (None: n_new) tokens completed, into the
+    pages' rows of digests [num_pages, 576] (bf16). Call it after the append."""
+    if not isinstance(seq_lens_before, torch.Tensor) or seq_lens_before.dim() != 1:
+        raise ValueError("seq_lens_before must be a tensor [B]")
+    B, dev = seq_lens_before.shape[0], seq_lens_before.device
+    pd = _need(digests, "digests", torch.bfloat16, (desc.num_pages, D_C + D_R))
+    _on(dev, pool=pool, digests=digests)
+    _call("mla_page_digest", dev, stream, ctypes.byref(desc), _pool(desc, pool), _table(block_table, B, dev),
+          block_table.shape[1], _ints(seq_lens_before, "seq_lens_before", (B,), dev),
+          _ints(new_lens, "new_lens", (B,), dev), int(n_new), pd, B)
+
+
+def new_digests(desc: mla_qcache_desc, device="cuda") -> torch.Tensor:
+    """Zeroed bf16 digests [num_pages, 576] of a pool's pages."""
+    return torch.zeros((desc.num_pages, D_C + D_R), dtype=torch.bfloat16, device=device)
+
+
+def _page_count(max_seq_len: int) -> int:
+    return -(-int(max_seq_len) // PAGE)
+
+
+def _queries(q_c, q_r):
+    if not isinstance(q_c, torch.Tensor) or q_c.dim() != 4:
+        raise ValueError("q_c must be a tensor [B, s_q, H, 512]")
+    B, s_q, H = q_c.shape[:3]
+    pc = _need(q_c, "q_c", torch.bfloat16, (B, s_q, H, D_C))
+    return B, s_q, H, pc, _need(q_r, "q_r", torch.bfloat16, (B, s_q, H, D_R))
+
+
+def mla_page_scores(block_table, seq_lens, max_seq_len, digests, q_c, q_r, scale, *, out=None, stream=None):
+    """Expected attention mass of every candidate page, fp32 [B, s_q, ceil(max_seq_len / 64)] (-inf
+    for pages that are no candidates). See include/mla_qcache.h."""
+    B, s_q, H, pc, pr = _queries(q_c, q_r)
+    dev = q_c.device
+    pd = _need(digests, "digests", torch.bfloat16)
+    if digests.dim() != 2 or digests.shape[1] != D_C + D_R:
+        raise ValueError(f"digests must have shape (num_pages, {D_C + D_R}), got {tuple(digests.shape)}")
+    shape = (B, s_q, _page_count(max_seq_len))
+    if out is None:
+        out = _empty(shape, torch.float32, dev, stream)
+    po = _need(out, "out", torch.float32, shape)
+    _on(dev, digests=digests, q_r=q_r, out=out)
+    _call("mla_page_scores", dev, stream, pd, digests.shape[0], _table(block_table, B, dev), block_table.shape[1],
+          _ints(seq_lens, "seq_lens", (B,), dev), int(max_seq_len), pc, pr, B, s_q, H, float(scale), po)
+    return out
+
+
+def mla_select_pages(block_table, seq_lens, max_seq_len, scores, k_pages, *, n_sink=1, n_recent=1, s_q=None,
+                     sel_table=None, sel_pages=None, sel_lens=None, stream=None):
+    """Pages each query attends: (sel_table [B, s_q, k_pages] pages of the pool, sel_pages their
+    indexes in the request, sel_lens [B, s_q] keys), int32, -1 behind the last page. scores
+    [B, s_q, ceil(max_seq_len / 64)] may be None when k_pages covers every page (then s_q is needed).
+    sel_table and sel_lens, flattened to B * s_q requests, are what mla_qdecode takes."""
+    if not isinstance(seq_lens, torch.Tensor) or seq_lens.dim() != 1:
+        raise ValueError("seq_lens must be a tensor [B]")
+    B, dev = seq_lens.shape[0], seq_lens.device
+    ps = None
+    if scores is not None:
+        if scores.dim() != 3:
+            raise ValueError("scores must be a tensor [B, s_q, pages]")
+        s_q = scores.shape[1]
+        ps = _need(scores, "scores", torch.float32, (B, s_q, _page_count(max_seq_len)))
+    elif s_q is None:
+        raise ValueError("s_q is needed without scores")
+    k = int(k_pages)
+    if sel_table is None:
+        sel_table = _empty((B, s_q, max(k, 0)), torch.int32, dev, stream)
+    if sel_pages is None:
+        sel_pages = _empty((B, s_q, max(k, 0)), torch.int32, dev, stream)
+    if sel_lens is None:
+        sel_lens = _empty((B, s_q), torch.int32, dev, stream)
+    _on(dev, scores=scores)
+    _call("mla_select_pages", dev, stream, _table(block_table, B, dev), block_table.shape[1],
+          _ints(seq_lens, "seq_lens", (B,), dev), int(max_seq_len), ps, B, s_q, k, int(n_sink), int(n_recent),
+          _ints(sel_table, "sel_table", (B, s_q, k), dev), _ints(sel_pages, "sel_pages", (B, s_q, k), dev),
+          _ints(sel_lens, "sel_lens", (B, s_q), dev))
+    return sel_table, sel_pages, sel_lens
+
+
+def mla_qdecode_sparse_workspace_bytes(B, s_q, H, max_seq_len, k_pages) -> int:
+    return int(_lib.load().mla_qdecode_sparse_workspace_bytes(B, s_q, H, int(max_seq_len), int(k_pages)))
+
+
+def mla_qdecode_sparse(desc, pool, block_table, seq_lens, max_seq_len, digests, q_c, q_r, scale, k_pages, *, n_sink=1,
+                       n_recent=1, out=None, out_dtype=torch.bfloat16, lse=None, workspace=None, flags=0, stream=None):
+    """One decode step over the pages that the digests' scores select (scores, selection, decode).
+    digests may be None when k_pages covers every page. Returns (out, lse). See include/mla_qcache.h."""
+    B, s_q, H, pc, pr = _queries(q_c, q_r)
+    dev = q_c.device
+    pd = None if digests is None else _need(digests, "digests", torch.bfloat16, (desc.num_pages, D_C + D_R))
+    if out is None:
+        out = _empty((B, s_q, H, D_C), out_dtype, dev, stream)
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out must be bfloat16 or float32")
+    po = _need(out, "out", out.dtype, (B, s_q, H, D_C))
+    pl = None if lse is None else _need(lse, "lse", torch.float32, (B, s_q, H))
+    if workspace is None:
+        workspace = _empty(max(mla_qdecode_sparse_workspace_bytes(B, s_q, H, max_seq_len, k_pages), 1), torch.uint8,
+                           dev, stream)
+    pw = _need(workspace, "workspace", torch.uint8)
+    _on(dev, pool=pool, digests=digests, q_r=q_r, out=out, lse=lse, workspace=workspace)
+    _call("mla_qdecode_sparse", dev, stream, ctypes.byref(desc), _pool(desc, pool), _table(block_table, B, dev),
+          block_table.shape[1], _ints(seq_lens, "seq_lens", (B,), dev), int(max_seq_len), pd, pc, pr, B, s_q, H,
+          float(scale), int(k_pages), int(n_sink), int(n_recent), pw, workspace.numel(), po,
+          int(out.dtype == torch.float32), pl, int(flags))
+    return out, lse
+
+
 def mla_cache_bytes_per_request(desc, seq_len, sink=0, window=0) -> int:
     """Bytes one request holds (desc None: the BF16 cache). See include/mla_qcache.h."""
     return int(_lib.load().mla_cache_bytes_per_request(None if desc is None else ctypes.byref(desc),

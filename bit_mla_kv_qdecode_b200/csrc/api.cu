@@ -148,6 +148,37 @@ HybridWorkspace hybrid_workspace(int B, int s_q, int H, int max_hist_len, int ma
   return w;
 }
 
+int page_count(int max_seq_len) { return static_cast<int>((static_cast<long>(max_seq_len) + mla::kPage - 1) / mla::kPage); }
+
+// Sparse decode workspace: scores, selection (table and lengths), then the
+// scratch of the decode over it, B * s_q requests of one query each. The
+// selection's rows are as wide as a query can need (n_sink + n_recent pages fit
+// there too: a query that sees no more than k_pages takes all of them).
+struct SparseWorkspace {
+  size_t off_scores, off_table, off_lens, off_inner, inner, total;
+  int k_pages, max_keys;
+};
+
+SparseWorkspace sparse_workspace(int B, int s_q, int H, int max_seq_len, int k_pages) {
+  const size_t queries = static_cast<size_t>(B) * s_q;
+  const int width = page_count(max_seq_len);
+  SparseWorkspace w{};
+  w.k_pages = k_pages;
+  w.max_keys = static_cast<int>(std::min<long>(static_cast<long>(k_pages) * mla::kPage, max_seq_len));
+  w.off_scores = 0;
+  w.off_table = align_up(k_pages < width ? queries * width * sizeof(float) : 0, 256);
+  w.off_lens = align_up(w.off_table + queries * w.k_pages * sizeof(int32_t), 256);
+  w.off_inner = align_up(w.off_lens + queries * sizeof(int32_t), 256);
+  w.inner = workspace_for(B * s_q, H, plan_splits(B * s_q, 1, H, w.max_keys, 0));
+  w.total = w.off_inner + w.inner;
+  return w;
+}
+
+bool valid_selection(int k_pages, int n_sink, int n_recent) {
+  return k_pages >= 1 && k_pages <= (1 << 20) && n_sink >= 0 && n_recent >= 1 &&
+         static_cast<long>(n_sink) + n_recent <= k_pages;
+}
+
 struct DecodeCommon {
   const void* pool;
   int num_pages;
@@ -473,6 +504,166 @@ mla_status mla_qdecode_hybrid(const mla_qcache_desc* desc, const void* pool, con
   r = run_decode(cp, false, nullptr);
   if (r != MLA_OK) return r;
   return from_cuda(mla::launch_merge2(o_hist, l_hist, o_prot, l_prot, B * s_q * H, out, out_dtype, lse, s));
+}
+
+mla_status mla_qcache_append_norm_rope(const mla_qcache_desc* desc, void* pool, const int32_t* block_table,
+                                       int max_pages_per_seq, const int32_t* seq_lens_before, const int32_t* new_lens,
+                                       const void* kv, int64_t kv_stride, const void* norm_weight, float eps,
+                                       const void* q, int64_t q_token_stride, int64_t q_head_stride, int H,
+                                       void* q_out, const float* cos_sin, int max_positions, const int32_t* positions,
+                                       int rope_pairs, void* rows_out, int B, int n_new, mla_stream_t stream) {
+  const mla_status st = mla_qcache_check_desc(desc);
+  if (st != MLA_OK) return st;
+  if (B < 0 || n_new < 0 || H < 0 || max_positions < 0) return MLA_ERR_INVALID_ARG;
+  if (!(eps > 0.0f) || !isfinite(eps)) return MLA_ERR_INVALID_ARG;
+  if (rope_pairs != MLA_ROPE_INTERLEAVED && rope_pairs != MLA_ROPE_HALF) return MLA_ERR_INVALID_ARG;
+  if (B == 0 || n_new == 0) return MLA_OK;
+  if (!pool || !block_table || !seq_lens_before || !kv || !cos_sin || max_pages_per_seq < 1)
+    return MLA_ERR_INVALID_ARG;
+  if ((H > 0) != (q != nullptr) || (H > 0) != (q_out != nullptr)) return MLA_ERR_INVALID_ARG;
+  if (kv_stride < 0 || kv_stride % 8 || q_token_stride < 0 || q_token_stride % 8 || q_head_stride < 0 ||
+      q_head_stride % 8)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned(pool, 256) || !aligned(kv, 16) || !aligned(norm_weight, 16) || !aligned(q, 16) || !aligned(q_out, 16) ||
+      !aligned(cos_sin, 16) || !aligned(rows_out, 16))
+    return MLA_ERR_INVALID_ARG;
+  const long tokens = static_cast<long>(B) * n_new;
+  if (tokens > (1L << 26) || H > 65536 || tokens * ((H + 31) / 32) > (1L << 30)) return MLA_ERR_UNSUPPORTED;
+  int* status = status_ptr();
+  if (!status) return MLA_ERR_CUDA;
+  mla::NormRopeLaunch L{pool, desc->num_pages, block_table, max_pages_per_seq, seq_lens_before, new_lens, kv,
+                        kv_stride, norm_weight, eps, q, q_token_stride, q_head_stride, H, q_out, cos_sin,
+                        max_positions, positions, rope_pairs == MLA_ROPE_HALF, rows_out, B, n_new, desc->bits_c,
+                        desc->group_c, desc->bits_r, desc->group_r, status, reinterpret_cast<cudaStream_t>(stream)};
+  return from_cuda(mla::launch_norm_rope_append(L));
+}
+
+mla_status mla_qcache_read(const mla_qcache_desc* desc, const void* pool, const int32_t* block_table,
+                           int max_pages_per_seq, const int32_t* start, const int32_t* cu_rows, int max_rows,
+                           int64_t total_rows, void* out_c, int64_t c_stride, void* out_kr, int64_t kr_stride, int B,
+                           mla_stream_t stream) {
+  const mla_status st = mla_qcache_check_desc(desc);
+  if (st != MLA_OK) return st;
+  if (B < 0 || max_rows < 0 || total_rows < 0) return MLA_ERR_INVALID_ARG;
+  if (B == 0 || max_rows == 0 || total_rows == 0) return MLA_OK;
+  if (!block_table || !cu_rows || max_pages_per_seq < 1 || (!out_c && !out_kr)) return MLA_ERR_INVALID_ARG;
+  if (desc->num_pages > 0 && !pool) return MLA_ERR_INVALID_ARG;
+  if (out_c && (c_stride < mla::kDc || c_stride % 8)) return MLA_ERR_INVALID_ARG;
+  if (out_kr && (kr_stride < mla::kDr || kr_stride % 8)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(pool, 256) || !aligned(out_c, 16) || !aligned(out_kr, 16)) return MLA_ERR_INVALID_ARG;
+  if (B > 65535) return MLA_ERR_UNSUPPORTED;
+  int* status = status_ptr();
+  if (!status) return MLA_ERR_CUDA;
+  mla::ReadLaunch L{pool, desc->num_pages, block_table, max_pages_per_seq, start, cu_rows, max_rows, total_rows, out_c,
+                    c_stride, out_kr, kr_stride, B, desc->bits_c, desc->group_c, desc->bits_r, desc->group_r, status,
+                    reinterpret_cast<cudaStream_t>(stream)};
+  return from_cuda(mla::launch_qcache_read(L));
+}
+
+mla_status mla_page_digest(const mla_qcache_desc* desc, const void* pool, const int32_t* block_table,
+                           int max_pages_per_seq, const int32_t* seq_lens_before, const int32_t* new_lens, int n_new,
+                           void* digests, int B, mla_stream_t stream) {
+  const mla_status st = mla_qcache_check_desc(desc);
+  if (st != MLA_OK) return st;
+  if (B < 0 || n_new < 0) return MLA_ERR_INVALID_ARG;
+  if (B == 0 || n_new == 0) return MLA_OK;
+  if (!block_table || !seq_lens_before || max_pages_per_seq < 1) return MLA_ERR_INVALID_ARG;
+  if (desc->num_pages > 0 && (!pool || !digests)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(pool, 256) || !aligned(digests, 16)) return MLA_ERR_INVALID_ARG;
+  if (B > 65535) return MLA_ERR_UNSUPPORTED;
+  int* status = status_ptr();
+  if (!status) return MLA_ERR_CUDA;
+  mla::DigestLaunch L{pool, desc->num_pages, block_table, max_pages_per_seq, seq_lens_before, new_lens, n_new, digests,
+                      B, desc->bits_c, desc->group_c, desc->bits_r, desc->group_r, status,
+                      reinterpret_cast<cudaStream_t>(stream)};
+  return from_cuda(mla::launch_page_digest(L));
+}
+
+mla_status mla_page_scores(const void* digests, int num_pages, const int32_t* block_table, int max_pages_per_seq,
+                           const int32_t* seq_lens, int max_seq_len, const void* q_c, const void* q_r, int B, int s_q,
+                           int H, float scale, float* scores, mla_stream_t stream) {
+  if (num_pages < 0 || B < 0 || s_q < 1 || H < 1 || max_seq_len < 0 || !isfinite(scale)) return MLA_ERR_INVALID_ARG;
+  if (B == 0 || max_seq_len == 0) return MLA_OK;
+  if (H > mla::kScoreHeads || static_cast<long>(B) * s_q > 65535) return MLA_ERR_UNSUPPORTED;
+  if (!block_table || !seq_lens || !q_c || !q_r || !scores || max_pages_per_seq < 1) return MLA_ERR_INVALID_ARG;
+  if (num_pages > 0 && !digests) return MLA_ERR_INVALID_ARG;
+  if (static_cast<long>(max_seq_len) > static_cast<long>(max_pages_per_seq) * mla::kPage) return MLA_ERR_CAPACITY;
+  if (!aligned(digests, 16) || !aligned(q_c, 16) || !aligned(q_r, 16) || !aligned(scores, 4))
+    return MLA_ERR_INVALID_ARG;
+  int* status = status_ptr();
+  if (!status) return MLA_ERR_CUDA;
+  mla::PageScoresLaunch L{digests, num_pages, block_table, max_pages_per_seq, seq_lens, max_seq_len, q_c, q_r, B, s_q,
+                          H, scale, scores, page_count(max_seq_len), status, reinterpret_cast<cudaStream_t>(stream)};
+  return from_cuda(mla::launch_page_scores(L));
+}
+
+mla_status mla_select_pages(const int32_t* block_table, int max_pages_per_seq, const int32_t* seq_lens,
+                            int max_seq_len, const float* scores, int B, int s_q, int k_pages, int n_sink,
+                            int n_recent, int32_t* sel_table, int32_t* sel_pages, int32_t* sel_lens,
+                            mla_stream_t stream) {
+  if (B < 0 || s_q < 1 || max_seq_len < 0 || !valid_selection(k_pages, n_sink, n_recent)) return MLA_ERR_INVALID_ARG;
+  if (B == 0) return MLA_OK;
+  if (static_cast<long>(B) * s_q > 65535) return MLA_ERR_UNSUPPORTED;
+  if (!block_table || !seq_lens || !sel_table || !sel_lens || max_pages_per_seq < 1) return MLA_ERR_INVALID_ARG;
+  if (!scores && k_pages < page_count(max_seq_len)) return MLA_ERR_INVALID_ARG;
+  if (static_cast<long>(max_seq_len) > static_cast<long>(max_pages_per_seq) * mla::kPage) return MLA_ERR_CAPACITY;
+  if (!aligned(scores, 4) || !aligned(sel_table, 4) || !aligned(sel_pages, 4) || !aligned(sel_lens, 4))
+    return MLA_ERR_INVALID_ARG;
+  int* status = status_ptr();
+  if (!status) return MLA_ERR_CUDA;
+  mla::PageSelectLaunch L{block_table, max_pages_per_seq, seq_lens, max_seq_len, scores, page_count(max_seq_len), B,
+                          s_q, k_pages, n_sink, n_recent, sel_table, sel_pages, sel_lens, status,
+                          reinterpret_cast<cudaStream_t>(stream)};
+  return from_cuda(mla::launch_page_select(L));
+}
+
+size_t mla_qdecode_sparse_workspace_bytes(int B, int s_q, int H, int max_seq_len, int k_pages) {
+  if (B <= 0 || s_q < 1 || H < 1 || max_seq_len < 0 || k_pages < 1) return 0;
+  if (static_cast<long>(B) * s_q > 65535 || H > (1 << 20)) return 0;
+  return sparse_workspace(B, s_q, H, max_seq_len, k_pages).total;
+}
+
+mla_status mla_qdecode_sparse(const mla_qcache_desc* desc, const void* pool, const int32_t* block_table,
+                              int max_pages_per_seq, const int32_t* seq_lens, int max_seq_len, const void* digests,
+                              const void* q_c, const void* q_r, int B, int s_q, int H, float scale, int k_pages,
+                              int n_sink, int n_recent, void* workspace, size_t workspace_bytes, void* out,
+                              int out_dtype, float* lse, unsigned flags, mla_stream_t stream) {
+  const mla_status st = mla_qcache_check_desc(desc);
+  if (st != MLA_OK) return st;
+  if (B < 0 || s_q < 1 || H < 1 || max_seq_len < 0 || !valid_selection(k_pages, n_sink, n_recent))
+    return MLA_ERR_INVALID_ARG;
+  if (out_dtype != 0 && out_dtype != 1) return MLA_ERR_INVALID_ARG;
+  if (!isfinite(scale) || (flags & ~(MLA_DECODE_FORCE_SIMT | MLA_DECODE_FAST_UNCOMPENSATED))) return MLA_ERR_INVALID_ARG;
+  if (B == 0) return MLA_OK;
+  const bool scored = k_pages < page_count(max_seq_len);
+  if (static_cast<long>(B) * s_q > 65535 || H > (1 << 20) || (scored && H > mla::kScoreHeads))
+    return MLA_ERR_UNSUPPORTED;
+  // everything the decode of the selection would refuse is refused before the first launch
+  if (!block_table || !seq_lens || !q_c || !q_r || !out || max_pages_per_seq < 1) return MLA_ERR_INVALID_ARG;
+  if (desc->num_pages > 0 && (!pool || (scored && !digests))) return MLA_ERR_INVALID_ARG;
+  if (!aligned(pool, 256) || !aligned(digests, 16) || !aligned(q_c, 16) || !aligned(q_r, 16) || !aligned(out, 16) ||
+      !aligned(lse, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (static_cast<long>(max_seq_len) > static_cast<long>(max_pages_per_seq) * mla::kPage) return MLA_ERR_CAPACITY;
+  const SparseWorkspace sw = sparse_workspace(B, s_q, H, max_seq_len, k_pages);
+  if (!workspace || workspace_bytes < sw.total || !aligned(workspace, 256)) return MLA_ERR_WORKSPACE;
+  char* base = static_cast<char*>(workspace);
+  float* scores = scored ? reinterpret_cast<float*>(base + sw.off_scores) : nullptr;
+  int32_t* sel_table = reinterpret_cast<int32_t*>(base + sw.off_table);
+  int32_t* sel_lens = reinterpret_cast<int32_t*>(base + sw.off_lens);
+  mla_status r = MLA_OK;
+  if (scored)
+    r = mla_page_scores(digests, desc->num_pages, block_table, max_pages_per_seq, seq_lens, max_seq_len, q_c, q_r, B,
+                        s_q, H, scale, scores, stream);
+  if (r != MLA_OK) return r;
+  r = mla_select_pages(block_table, max_pages_per_seq, seq_lens, max_seq_len, scores, B, s_q, sw.k_pages, n_sink,
+                       n_recent, sel_table, nullptr, sel_lens, stream);
+  if (r != MLA_OK) return r;
+  // B * s_q requests of one query each, over their own tables
+  DecodeCommon c{pool, desc->num_pages, sel_table, sw.k_pages, sel_lens, sw.max_keys, q_c, q_r, B * s_q, 1, H, scale, 0,
+                 sw.inner ? base + sw.off_inner : nullptr, sw.inner, out, out_dtype, lse, flags,
+                 reinterpret_cast<cudaStream_t>(stream)};
+  return run_decode(c, true, desc);
 }
 
 size_t mla_cache_bytes_per_request(const mla_qcache_desc* desc, long seq_len, int sink, int window) {

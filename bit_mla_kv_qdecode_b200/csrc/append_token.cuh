@@ -32,23 +32,17 @@ __device__ __forceinline__ void group_params(float mn, float mx, __half& s16, __
   z16 = __float2half_rn(mn);
 }
 
-// Writes token (c_src [512], kr_src [64], bf16) into slot `slot` of page `pg`:
-// content codes, content (s,z), RoPE codes, RoPE (s,z). All 32 lanes call it.
-template <int BITS_C, int G_C, int BITS_R, int G_R>
-__device__ __forceinline__ void quantize_token_warp(uint8_t* pg, int slot, const __nv_bfloat16* c_src,
-                                                    const __nv_bfloat16* kr_src, int lane) {
+// Writes one token into slot `slot` of page `pg`: content codes, content (s,z),
+// RoPE codes, RoPE (s,z). Lane l holds content channels [16l, 16l+16) in x and
+// RoPE channels {2l, 2l+1} in r0, r1 (bf16 values). With kHat, x, r0 and r1 are
+// replaced by the values the written codes stand for, u*s + z (u*s is exact in
+// fp32, so the sum is the one rounding). All 32 lanes call it.
+template <int BITS_C, int G_C, int BITS_R, int G_R, bool kHat>
+__device__ __forceinline__ void quantize_values_warp(uint8_t* pg, int slot, float (&x)[16], float& r0, float& r1,
+                                                     int lane) {
   using G = QGeom<BITS_C, G_C, BITS_R, G_R>;
 
   // ---- content path: 16 channels per lane ----
-  const uint4* src = reinterpret_cast<const uint4*>(c_src) + 2 * lane;
-  const uint4 v0 = __ldg(src), v1 = __ldg(src + 1);
-  const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-  float x[16];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    x[2 * k] = bf16_lo(w[k]);
-    x[2 * k + 1] = bf16_hi(w[k]);
-  }
   float mn = x[0], mx = x[0];
 #pragma unroll
   for (int k = 1; k < 16; ++k) {
@@ -70,6 +64,7 @@ __device__ __forceinline__ void quantize_token_warp(uint8_t* pg, int slot, const
     const uint32_t u = quantize_code<BITS_C>(x[k], s, z);
     const int bit = k * BITS_C;
     packed[bit >> 5] |= u << (bit & 31);
+    if constexpr (kHat) x[k] = __fmaf_rn(static_cast<float>(u), s, z);
   }
   uint8_t* crow = pg + G::kOffCC + slot * G::kRowC;
   if constexpr (BITS_C == 4) {
@@ -84,8 +79,6 @@ __device__ __forceinline__ void quantize_token_warp(uint8_t* pg, int slot, const
   }
 
   // ---- RoPE path: 2 channels per lane ----
-  const uint32_t rw = __ldg(reinterpret_cast<const uint32_t*>(kr_src) + lane);
-  const float r0 = bf16_lo(rw), r1 = bf16_hi(rw);
   float rmn = fminf(r0, r1), rmx = fmaxf(r0, r1);
   constexpr int kLanesR = G_R / 2;
 #pragma unroll
@@ -96,7 +89,12 @@ __device__ __forceinline__ void quantize_token_warp(uint8_t* pg, int slot, const
   __half rs16, rz16;
   group_params<BITS_R>(rmn, rmx, rs16, rz16);
   const float rs = __half2float(rs16), rz = __half2float(rz16);
-  const uint32_t rbits = quantize_code<BITS_R>(r0, rs, rz) | (quantize_code<BITS_R>(r1, rs, rz) << BITS_R);
+  const uint32_t u0 = quantize_code<BITS_R>(r0, rs, rz), u1 = quantize_code<BITS_R>(r1, rs, rz);
+  const uint32_t rbits = u0 | (u1 << BITS_R);
+  if constexpr (kHat) {
+    r0 = __fmaf_rn(static_cast<float>(u0), rs, rz);
+    r1 = __fmaf_rn(static_cast<float>(u1), rs, rz);
+  }
   uint8_t* rrow = pg + G::kOffRC + slot * G::kRowR;
   if constexpr (BITS_R == 4) {
     rrow[lane] = static_cast<uint8_t>(rbits);
@@ -109,6 +107,25 @@ __device__ __forceinline__ void quantize_token_warp(uint8_t* pg, int slot, const
                           (static_cast<uint32_t>(__half_as_ushort(rz16)) << 16);
     reinterpret_cast<uint32_t*>(pg + G::kOffRM + slot * G::kGroupsR * 4)[lane / kLanesR] = meta;
   }
+}
+
+// Writes token (c_src [512], kr_src [64], bf16) into slot `slot` of page `pg`.
+// All 32 lanes call it.
+template <int BITS_C, int G_C, int BITS_R, int G_R>
+__device__ __forceinline__ void quantize_token_warp(uint8_t* pg, int slot, const __nv_bfloat16* c_src,
+                                                    const __nv_bfloat16* kr_src, int lane) {
+  const uint4* src = reinterpret_cast<const uint4*>(c_src) + 2 * lane;
+  const uint4 v0 = __ldg(src), v1 = __ldg(src + 1);
+  const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+  float x[16];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    x[2 * k] = bf16_lo(w[k]);
+    x[2 * k + 1] = bf16_hi(w[k]);
+  }
+  const uint32_t rw = __ldg(reinterpret_cast<const uint32_t*>(kr_src) + lane);
+  float r0 = bf16_lo(rw), r1 = bf16_hi(rw);
+  quantize_values_warp<BITS_C, G_C, BITS_R, G_R, false>(pg, slot, x, r0, r1, lane);
 }
 
 }  // namespace mla

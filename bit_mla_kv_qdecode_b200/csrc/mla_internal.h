@@ -27,6 +27,22 @@ cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, size
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
+// Return fn<bits_c, group_c, bits_r, group_r>(...) for the cache format of launch description L
+// (falls through when the format is none of the sixteen).
+#define MLA_FORMAT_CASE(L, fn, BC, GC, BR, GR, ...)                                            \
+  if ((L).bits_c == BC && (L).group_c == GC && (L).bits_r == BR && (L).group_r == GR)        \
+    return fn<BC, GC, BR, GR>(__VA_ARGS__);
+#define MLA_FORMAT_CASES_R(L, fn, BC, GC, ...)                                                  \
+  MLA_FORMAT_CASE(L, fn, BC, GC, 4, 64, __VA_ARGS__)                                            \
+  MLA_FORMAT_CASE(L, fn, BC, GC, 4, 32, __VA_ARGS__)                                            \
+  MLA_FORMAT_CASE(L, fn, BC, GC, 2, 64, __VA_ARGS__)                                            \
+  MLA_FORMAT_CASE(L, fn, BC, GC, 2, 32, __VA_ARGS__)
+#define MLA_FORMAT_DISPATCH(L, fn, ...)                                                         \
+  MLA_FORMAT_CASES_R(L, fn, 4, 64, __VA_ARGS__)                                                 \
+  MLA_FORMAT_CASES_R(L, fn, 4, 32, __VA_ARGS__)                                                 \
+  MLA_FORMAT_CASES_R(L, fn, 2, 64, __VA_ARGS__)                                                 \
+  MLA_FORMAT_CASES_R(L, fn, 2, 32, __VA_ARGS__)
+
 struct AppendLaunch {
   void* pool;
   int num_pages;
@@ -51,6 +67,108 @@ struct AppendLaunch {
 
 cudaError_t launch_qcache_append(const AppendLaunch& L);
 cudaError_t launch_bf16cache_append(const AppendLaunch& L);
+
+// Norm + rotation + quantized append of new tokens, and the rotation of their queries.
+struct NormRopeLaunch {
+  void* pool;
+  int num_pages;
+  const int32_t* table;
+  int max_pages;
+  const int32_t* lens_before;
+  const int32_t* new_lens;  // or null: every request has n_new tokens
+  const void* kv;           // bf16 rows [B * n_new], kv_stride elements apart
+  int64_t kv_stride;
+  const void* norm_weight;  // bf16 [512] or null
+  float eps;
+  const void* q;            // bf16; (token, head) at token * q_token_stride + head * q_head_stride
+  int64_t q_token_stride, q_head_stride;
+  int H;                    // 0: no queries
+  void* q_out;              // bf16 [B * n_new, H, 64]
+  const float* cos_sin;     // [max_positions][64]
+  int max_positions;
+  const int32_t* positions;  // [B * n_new] or null
+  int half_pairs;
+  void* rows_out;  // bf16 [B * n_new, 576] or null
+  int B, n_new;
+  int bits_c, group_c, bits_r, group_r;
+  int* status;
+  cudaStream_t stream;
+};
+cudaError_t launch_norm_rope_append(const NormRopeLaunch& L);
+
+// Dequantized rows of a token range of every request.
+struct ReadLaunch {
+  const void* pool;
+  int num_pages;
+  const int32_t* table;
+  int max_pages;
+  const int32_t* start;  // or null: 0
+  const int32_t* cu_rows;
+  int max_rows;
+  int64_t total_rows;
+  void* out_c;
+  int64_t c_stride;
+  void* out_kr;
+  int64_t kr_stride;
+  int B;
+  int bits_c, group_c, bits_r, group_r;
+  int* status;
+  cudaStream_t stream;
+};
+cudaError_t launch_qcache_read(const ReadLaunch& L);
+
+// Mean keys of the pages that an append completed.
+struct DigestLaunch {
+  const void* pool;
+  int num_pages;
+  const int32_t* table;
+  int max_pages;
+  const int32_t* lens_before;
+  const int32_t* new_lens;  // or null: n_new each
+  int n_new;
+  void* digests;
+  int B;
+  int bits_c, group_c, bits_r, group_r;
+  int* status;
+  cudaStream_t stream;
+};
+cudaError_t launch_page_digest(const DigestLaunch& L);
+
+// Scores of the candidate pages, and the selection by them.
+struct PageScoresLaunch {
+  const void* digests;
+  int num_pages;
+  const int32_t* table;
+  int max_pages;
+  const int32_t* seq_lens;
+  int max_seq_len;
+  const void* q_c;
+  const void* q_r;
+  int B, s_q, H;
+  float scale;
+  float* scores;  // [B, s_q, width]
+  int width;
+  int* status;
+  cudaStream_t stream;
+};
+constexpr int kScoreHeads = 128;  // most heads a scores call takes
+cudaError_t launch_page_scores(const PageScoresLaunch& L);
+
+struct PageSelectLaunch {
+  const int32_t* table;
+  int max_pages;
+  const int32_t* seq_lens;
+  int max_seq_len;
+  const float* scores;  // [B, s_q, width]; null when k_pages >= width
+  int width;
+  int B, s_q, k_pages, n_sink, n_recent;
+  int32_t* sel_table;
+  int32_t* sel_pages;  // or null
+  int32_t* sel_lens;
+  int* status;
+  cudaStream_t stream;
+};
+cudaError_t launch_page_select(const PageSelectLaunch& L);
 
 // One decode call, after validation and split planning.
 struct DecodeLaunch {

@@ -349,6 +349,171 @@ mla_status mla_qdecode_hybrid(const mla_qcache_desc* desc, const void* pool,
                               void* workspace, size_t workspace_bytes,
                               void* out, int out_dtype, float* lse, mla_stream_t stream);
 
+/* ---- Writing from the projections, reading back ---- */
+
+/* Rotary pairs of mla_qcache_append_norm_rope: channels (2i, 2i+1), or (i, i+32). */
+#define MLA_ROPE_INTERLEAVED 0
+#define MLA_ROPE_HALF 1
+
+/* mla_qcache_append from the raw projections, in one launch: RMS norm of the
+ * latent, rotation of the decoupled key and of every head's decoupled query,
+ * then the quantizer and the paged write. For token j of request b, with
+ * x = kv row [0, 512), r = kv row [512, 576) and the angle of its position:
+ *   c  = bf16(x / sqrt(mean(x^2) + eps) * w),  k_r = bf16(rotate(r)),
+ *   q_out[b,j,h,:] = bf16(rotate(q[b,j,h,:])),
+ *   rotate: (a, b) -> (a cos - b sin, a sin + b cos) on each rotary pair,
+ * and the cache slot of position seq_lens_before[b] + j gets the bytes that
+ * mla_qcache_append writes for c and k_r. The norm and the key's rotation are
+ * computed in fp64 and rounded to fp32, then bf16, so that the codes are
+ * reproducible; the queries' rotation is computed in fp32.
+ *   desc, pool, block_table, max_pages_per_seq, seq_lens_before
+ *                   as for mla_qcache_append.
+ *   new_lens        device int32 [B] or NULL: tokens given of request b, in
+ *                   [0, n_new]; the padding behind them is neither read nor
+ *                   written (NULL: n_new each).
+ *   kv              device bf16, row b * n_new + j at kv + row * kv_stride
+ *                   elements: 512 latent channels, then 64 of the key (a column
+ *                   range of a fused projection's output will do).
+ *   norm_weight     device bf16 [512], or NULL (w = 1).
+ *   eps             > 0, finite.
+ *   q               device bf16, head h of row r at
+ *                   q + r * q_token_stride + h * q_head_stride, 64 channels; NULL
+ *                   with H = 0 when there are no queries to rotate.
+ *   q_out           device bf16 [B, n_new, H, 64], dense. May be q itself when q
+ *                   is dense too; otherwise the two must not overlap.
+ *   cos_sin         device fp32 [max_positions, 64]: 32 cosines, then 32 sines,
+ *                   of the rotary pairs at each position.
+ *   positions       device int32 [B, n_new] or NULL (the cache position).
+ *   rope_pairs      MLA_ROPE_INTERLEAVED or MLA_ROPE_HALF.
+ *   rows_out        device bf16 [B, n_new, 576] or NULL: the values the cache
+ *                   now holds for these tokens, c_hat then kr_hat, so that a
+ *                   prefill attends to what later decodes will see.
+ * Every pointer to bf16 and cos_sin is 16-byte aligned; strides are
+ * non-negative multiples of 8 elements. A token whose angle position is outside
+ * [0, max_positions) is skipped and flagged; a cache position past the table
+ * row or a table entry outside the pool skips the token's slot and its
+ * rows_out row, and is flagged. B == 0 or n_new == 0 is a no-op. */
+mla_status mla_qcache_append_norm_rope(const mla_qcache_desc* desc, void* pool,
+                                       const int32_t* block_table, int max_pages_per_seq,
+                                       const int32_t* seq_lens_before, const int32_t* new_lens,
+                                       const void* kv, int64_t kv_stride,
+                                       const void* norm_weight, float eps,
+                                       const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                       int H, void* q_out,
+                                       const float* cos_sin, int max_positions,
+                                       const int32_t* positions, int rope_pairs, void* rows_out,
+                                       int B, int n_new, mla_stream_t stream);
+
+/* Dequantized rows of the quantized cache: tokens start[b] + i, for i below
+ * cu_rows[b+1] - cu_rows[b], of request b go to row cu_rows[b] + i.
+ *   desc, pool, block_table, max_pages_per_seq   as for mla_qcache_append.
+ *   start        device int32 [B] or NULL (0 each).
+ *   cu_rows      device int32 [B+1], not decreasing: the first row of each
+ *                request, and the end.
+ *   max_rows     host upper bound on the rows of one request.
+ *   total_rows   rows that the outputs have room for.
+ *   out_c        device bf16 [total_rows, 512] with row stride c_stride
+ *                (elements), or NULL; out_kr the same, 64 wide, kr_stride. The
+ *                two may be column ranges of one buffer. 16-byte aligned;
+ *                strides are multiples of 8, at least the width.
+ * Values are bf16(u * s + z). A request whose rows exceed max_rows or the
+ * outputs is cut there and flagged; tokens at bad positions or pages are
+ * skipped (their rows are left as they were) and flagged. Rows outside every
+ * request's range are left as they were. */
+mla_status mla_qcache_read(const mla_qcache_desc* desc, const void* pool,
+                           const int32_t* block_table, int max_pages_per_seq,
+                           const int32_t* start, const int32_t* cu_rows, int max_rows, int64_t total_rows,
+                           void* out_c, int64_t c_stride, void* out_kr, int64_t kr_stride,
+                           int B, mla_stream_t stream);
+
+/* ---- Sparse decode: attention over the pages a cheap score selects ----
+ *
+ * A complete page is represented by its digest, the mean of its 64 dequantized
+ * keys [c_hat | kr_hat] (576 bf16 values, 1,152 B beside the page's 14,592 to
+ * 24,832). Candidates of query i of request b, with L = seq_lens[b] - s_q + 1 + i
+ * visible keys, are the pages before its own: p < P = floor((L - 1) / 64), all of them
+ * complete and older than the query. Their score is the attention mass they would hold
+ * if every key were its page's mean, summed over the heads, which share a
+ * selection because they share the cache:
+ *   S[h,p] = scale * (q_c[h] . d_c[p] + q_r[h] . d_r[p]),
+ *   score[p] = sum_h exp(S[h,p]) / sum_{p'<P} exp(S[h,p']).
+ * The query then attends the first n_sink pages, the newest n_recent pages (its
+ * own one among them), and the candidates with the highest scores, k_pages in
+ * all. */
+
+/* Digests of the pages that an append of tokens completed: for request b every
+ * page p with seq_lens_before[b] / 64 <= p < (seq_lens_before[b] + n_b) / 64,
+ * n_b = new_lens[b] (or n_new for NULL). Call it after the append, on its stream.
+ *   desc, pool, block_table, max_pages_per_seq, seq_lens_before  as for
+ *                mla_qcache_append; new_lens, n_new as for
+ *                mla_qcache_append_norm_rope.
+ *   digests      device bf16 [num_pages, 576], 16-byte aligned, by page of the
+ *                pool; only the completed pages' rows are written.
+ * Sums are fp32. Requests with a length outside these bounds and pages outside
+ * the pool are skipped and flagged. */
+mla_status mla_page_digest(const mla_qcache_desc* desc, const void* pool,
+                           const int32_t* block_table, int max_pages_per_seq,
+                           const int32_t* seq_lens_before, const int32_t* new_lens, int n_new,
+                           void* digests, int B, mla_stream_t stream);
+
+/* Scores of the candidate pages, as above.
+ *   digests      device bf16 [num_pages, 576], 16-byte aligned.
+ *   block_table, max_pages_per_seq, seq_lens, max_seq_len, q_c, q_r, B, s_q, H,
+ *   scale        as for mla_qdecode; H <= 128.
+ *   scores       device fp32 [B, s_q, W], W = ceil(max_seq_len / 64); -inf for
+ *                pages that are no candidates.
+ * A candidate whose table entry is outside the pool scores -inf, takes no part
+ * in the softmax, and is flagged. */
+mla_status mla_page_scores(const void* digests, int num_pages,
+                           const int32_t* block_table, int max_pages_per_seq,
+                           const int32_t* seq_lens, int max_seq_len,
+                           const void* q_c, const void* q_r, int B, int s_q, int H, float scale,
+                           float* scores, mla_stream_t stream);
+
+/* The pages each query attends, in position order.
+ *   scores       device fp32 [B, s_q, W], W = ceil(max_seq_len / 64); may be
+ *                NULL when k_pages >= W. Equal scores: the lower page first. NaN
+ *                ranks below every number.
+ *   k_pages      pages a query attends at most; n_sink >= 0, n_recent >= 1,
+ *                n_sink + n_recent <= k_pages. A query that sees no more than
+ *                k_pages attends all of them.
+ *   sel_table    device int32 [B, s_q, k_pages]: pages of the pool, as
+ *                block_table has them; -1 behind the last.
+ *   sel_pages    device int32, the same shape, or NULL: their indexes in the
+ *                request; -1 behind the last.
+ *   sel_lens     device int32 [B, s_q]: keys they hold that the query sees (only
+ *                the last page can be partly filled); 0 when it sees none.
+ * (sel_table, sel_lens) are the block table and lengths of B * s_q requests of
+ * one query each: mla_qdecode over them is the sparse decode. */
+mla_status mla_select_pages(const int32_t* block_table, int max_pages_per_seq,
+                            const int32_t* seq_lens, int max_seq_len, const float* scores,
+                            int B, int s_q, int k_pages, int n_sink, int n_recent,
+                            int32_t* sel_table, int32_t* sel_pages, int32_t* sel_lens,
+                            mla_stream_t stream);
+
+/* Workspace bytes mla_qdecode_sparse needs (0 for invalid arguments). Host only. */
+size_t mla_qdecode_sparse_workspace_bytes(int B, int s_q, int H, int max_seq_len, int k_pages);
+
+/* One decode step over the selected pages: mla_page_scores, mla_select_pages
+ * and mla_qdecode (library split plan) of the selection, on one stream. When
+ * k_pages covers every page the scores are not computed, and H is not limited.
+ *   digests      as for mla_page_scores (num_pages = desc's); may be NULL when
+ *                k_pages >= ceil(max_seq_len / 64).
+ *   workspace    device, 256-byte aligned, at least
+ *                mla_qdecode_sparse_workspace_bytes(...) bytes; calls that may
+ *                overlap need one each.
+ *   other arguments as for mla_qdecode and mla_select_pages; B * s_q <= 65535.
+ * Output, lse and errors as for mla_qdecode, over the selected keys. */
+mla_status mla_qdecode_sparse(const mla_qcache_desc* desc, const void* pool,
+                              const int32_t* block_table, int max_pages_per_seq,
+                              const int32_t* seq_lens, int max_seq_len, const void* digests,
+                              const void* q_c, const void* q_r,
+                              int B, int s_q, int H, float scale,
+                              int k_pages, int n_sink, int n_recent,
+                              void* workspace, size_t workspace_bytes,
+                              void* out, int out_dtype, float* lse,
+                              unsigned flags, mla_stream_t stream);
+
 /* ---- Cache capacity (host arithmetic, no device work) ----
  *
  * Bytes one request of seq_len tokens holds in whole pages: the quantized
