@@ -1,8 +1,41 @@
-// Expected attention mass of each candidate page of a query:
+// Expected attention mass of each candidate page of a query, on the tensor cores:
 //   S[h, p]  = scale * (q_h . kbar_p),  kbar_p the page's mean key
-//   mass[p]  = sum_h softmax_p(S[h, :])[p]
-// over the complete pages before the query's own one.
+//   mass[p]  = sum_h exp(S[h, p]) / sum_p' exp(S[h, p'])
+// over the complete pages p before the query's own one.
+//
+// A cluster of C CTAs takes one query; tile t of 128 pages goes to CTA t mod C.
+// Heads are the MMA's M side (one TMEM lane a head), pages its N side, so a
+// head's maximum and sum run along its lane's own columns, with no exchange
+// between lanes; only the last sum, over heads, crosses lanes. A CTA keeps the
+// logits of two tiles in tensor memory: up to 2 * C tiles (131,072 tokens at 8
+// CTAs) the statistics of the whole query are known before any logit is read
+// again, and none goes through memory. A longer query's tiles are computed
+// twice, first for the statistics. (Pages as the M side, with the statistics
+// reduced across lanes, took 3.7 us a tile of 128 heads instead of 0.5.)
+//
+// Precision. The tensor cores' fp32 accumulation truncates, in proportion to
+// the sum so far and to the steps: with one accumulator for all 576 channels
+// the scores of pages that hold most of the mass were off by 2e-6. A logit is
+// therefore summed in three accumulators of 192 channels each, added in fp32.
+// The first is the tile's own; the other two are scratch that every tile uses
+// and that is free again once the statistics pass has added the three up.
+//
+// Digests are gathered by the block table with 16-byte asynchronous copies into
+// the swizzled operand layout, 64 channels of 128 pages a stage; the query's
+// heads come with nine tiled loads and stay for all tiles. (TMA's gather of four
+// rows a request moved 10 GB/s an SM at 128 bytes a row, these copies 43.)
+// Warp roles:
+//   warps 0-15   a quarter of the heads and a quarter of a tile's pages each:
+//                statistics, later weights and their sum over the heads
+//   warps 16-19  copies
+//   warp 20      tensor memory, MMA issue
+// The CTAs' statistics meet in distributed shared memory, in rank order, so
+// results do not depend on timing. Every wait is bounded; one that runs out
+// sets MLA_ERR_TIMEOUT and leaves the scores undefined.
+#include <cuda.h>
 #include <math_constants.h>
+
+#include <mutex>
 
 #include "mla_common.cuh"
 #include "mla_internal.h"
@@ -11,94 +44,486 @@
 namespace mla {
 namespace {
 
+constexpr int kSoftWarps = 16, kCopyWarps = 4;
+constexpr int kSoftThreads = kSoftWarps * 32;
+constexpr int kThreads = (kSoftWarps + kCopyWarps + 1) * 32;
+constexpr int kTile = 128;                         // pages of a tile
+constexpr int kBlockCh = 64;                       // channels of one operand stage (128 B a row)
+constexpr int kBlocks = kDqk / kBlockCh;           // 9: eight of the content, one of the RoPE part
+constexpr int kStageBytes = kTile * kBlockCh * 2;  // 16 KB
+constexpr int kQBlock = kScoreHeads * kBlockCh * 2;
+constexpr int kStages = 4;
+constexpr int kAccs = 3;                           // accumulators of a logit
+constexpr int kAccBlocks = kBlocks / kAccs;
+constexpr int kHeld = 2;                           // tiles whose logits tensor memory holds
+constexpr uint32_t kScratchCol = kHeld * kTile;
+constexpr uint32_t kTmemCols = 512;
+static_assert(kAccs == 3 && kHeld == 2 && kBlocks % kAccs == 0 && (kHeld + kAccs - 1) * kTile <= static_cast<int>(kTmemCols), "accumulators");
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr int kSmemLimit = 232448;
+
 struct ScoreArgs {
-  const __nv_bfloat16* digests;
+  const __nv_bfloat16* digests;  // [num_pages][576]
   const int32_t* table;
   const int32_t* seq_lens;
-  const __nv_bfloat16* q_c;
-  const __nv_bfloat16* q_r;
   float* scores;
   int* status;
   int num_pages, max_pages, max_seq_len, s_q, H, width;
   float scale_log2;
 };
 
-__device__ float block_reduce(float v, bool is_max, float* buf) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float u = __shfl_xor_sync(0xffffffffu, v, o);
-    v = is_max ? fmaxf(v, u) : v + u;
-  }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = buf[0];
-  for (int w = 1; w < 8; ++w) v = is_max ? fmaxf(v, buf[w]) : v + buf[w];
+struct Maps {
+  CUtensorMap q_c;  // bf16 [B * s_q * H][512], box 64 x H
+  CUtensorMap q_r;  // bf16 [B * s_q * H][64], box 64 x H
+};
+
+struct Misc {
+  uint64_t full[kStages], empty[kStages], q_full[kBlocks], t_full[kHeld], t_empty[kHeld], scratch_empty;
+  float2 part[4][kScoreHeads];  // (maximum, sum) of each head over a quarter of the CTA's pages
+  float2 cta[kScoreHeads];      // over the CTA's pages
+  float mass[2][4][kTile];      // a tile's weights, summed over a quarter of the heads
+  uint32_t tmem;
+  int abort;
+};
+constexpr int kSmemBytes = kStages * kStageBytes + kBlocks * kQBlock + static_cast<int>(sizeof(Misc)) + 1024;
+static_assert(kSmemBytes <= kSmemLimit, "shared memory budget");
+static_assert(kSmemBytes > kSmemLimit / 2, "one CTA per SM keeps the 512-column TMEM allocation uncontended");
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Arrive on `bar` when this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const void* tmap, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          ptx::smem_u32(dst)),
+      "l"(tmap), "r"(x), "r"(y), "r"(ptx::smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
 }
 
-__global__ void __launch_bounds__(256) page_scores_kernel(const ScoreArgs a) {
+// K-major operand of 128-byte rows in the 128-byte swizzle: 8-row groups 1,024 B apart.
+__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); }
+
+// Fold (top, sum) of another part into (m, l): sums of 2^(x - maximum).
+__device__ __forceinline__ void fold(float& m, float& l, float top, float sum) {
+  const float up = fmaxf(m, top);
+  if (up == -CUDART_INF_F) return;
+  l = fmaf(l, exp2_approx(m - up), sum * exp2_approx(top - up));
+  m = up;
+}
+
+// Sum each of 32 columns over the warp's lanes; lane l returns column l's.
+__device__ __forceinline__ float sum_columns(float (&v)[32], int lane) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int k = 0; k < s; ++k) {
+      const float keep = up ? v[s + k] : v[k], give = up ? v[k] : v[s + k];
+      v[k] = keep + __shfl_xor_sync(0xffffffffu, give, s);
+    }
+  }
+  return v[0];
+}
+
+__global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArgs a, const __grid_constant__ Maps maps) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (ptx::smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* ring = smem;
+  uint8_t* qbuf = ring + kStages * kStageBytes;
+  Misc& m = *reinterpret_cast<Misc*>(qbuf + kBlocks * kQBlock);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(ptx::cluster_ctarank());
+  int C;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(C));
+  const int unit = blockIdx.x / C, b = unit / a.s_q, i = unit - b * a.s_q;
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&m.full[s], kCopyWarps * 32);
+      ptx::mbar_init(&m.empty[s], 1);
+    }
+    for (int k = 0; k < kBlocks; ++k) ptx::mbar_init(&m.q_full[k], 1);
+    for (int t = 0; t < kHeld; ++t) {
+      ptx::mbar_init(&m.t_full[t], 1);
+      ptx::mbar_init(&m.t_empty[t], kSoftWarps);
+    }
+    ptx::mbar_init(&m.scratch_empty, kSoftWarps);
+    m.abort = 0;
+    ptx::fence_mbar_init_cluster();
+  }
+  if (warp == kSoftWarps + kCopyWarps) {
+    ptx::tmem_alloc(&m.tmem, kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  if (tid == kSoftThreads) {
+    ptx::prefetch_tmap(&maps.q_c);
+    ptx::prefetch_tmap(&maps.q_r);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = m.tmem;
   ptx::griddep_wait();
-  ptx::griddep_launch_dependents();
-  extern __shared__ float smem[];
-  __shared__ float q[kDqk], buf[8];
-  float* s = smem;
-  float* mass = smem + a.width;
-  const int b = blockIdx.y, i = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
   int T = __ldg(a.seq_lens + b);
   if (T < 0 || T > a.max_seq_len) {
-    if (tid == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
+    if (tid == 0 && rank == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
     T = T < 0 ? 0 : a.max_seq_len;
   }
   const int L = T - a.s_q + 1 + i, P = L > 0 ? (L - 1) / kPage : 0;
-  for (int p = tid; p < P; p += 256) mass[p] = 0.0f;
-  for (int h = 0; h < a.H; ++h) {
-    const size_t row = (static_cast<size_t>(b) * a.s_q + i) * a.H + h;
-    __syncthreads();
-    for (int c = tid; c < kDqk; c += 256)
-      q[c] = __bfloat162float(c < kDc ? a.q_c[row * kDc + c] : a.q_r[row * kDr + c - kDc]);
-    __syncthreads();
-    float m = -CUDART_INF_F;
-    for (int p = warp; p < P; p += 8) {
-      const int page = lookup_page(a.table, a.max_pages, a.num_pages, b, p * kPage);
-      float dot = 0.0f;
-      if (page >= 0)
-        for (int c = lane; c < kDqk; c += 32)
-          dot = fmaf(q[c], __bfloat162float(a.digests[static_cast<size_t>(page) * kDqk + c]), dot);
+  const int tiles = (P + kTile - 1) / kTile;
+  const int mine = a.num_pages > 0 && tiles > rank ? (tiles - 1 - rank) / C + 1 : 0;
+  const bool twice = mine > kHeld;
+  volatile int* abort_flag = &m.abort;
+  auto give_up = [&] {
+    *abort_flag = 1;
+    record_error(a.status, MLA_ERR_TIMEOUT);
+  };
+  // A whole warp waits; when one lane's wait runs out, all of them leave together.
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort_flag, kWaitLimitNs));
+    if (!ok) give_up();
+    return ok;
+  };
+  auto page_of = [&](int p) -> int {
+    return p < P ? lookup_page(a.table, a.max_pages, a.num_pages, b, p * kPage) : -1;
+  };
+  auto tile_of = [&](int n) { return rank + (n < mine ? n : n - mine) * C; };  // n counts over both sweeps
+
+  // Copy the digests of this CTA's tiles into the ring. Eight lanes take one
+  // page's 128 bytes of a stage, a warp 32 pages.
+  auto produce = [&](int n0, int n1) {
+    const int w = warp - kSoftWarps, sub = lane >> 3, chunk = lane & 7;
+    auto lane_page = [&](int n) {  // pages that are none read page 0; their logits are masked
+      return n < n1 ? max(page_of(tile_of(n) * kTile + 32 * w + lane), 0) : 0;
+    };
+    int next = lane_page(n0);
+    for (int n = n0; n < n1; ++n) {
+      const uint8_t* src[8];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if (page < 0 && lane == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
-      const float v = page >= 0 ? dot * a.scale_log2 : -CUDART_INF_F;
-      if (lane == 0) s[p] = v;
-      m = fmaxf(m, v);
+      for (int j = 0; j < 8; ++j) {
+        const int page = __shfl_sync(0xffffffffu, next, 4 * j + sub);
+        src[j] = reinterpret_cast<const uint8_t*>(a.digests + static_cast<size_t>(page) * kDqk) + 16 * chunk;
+      }
+      next = lane_page(n + 1);
+      for (int k = 0; k < kBlocks; ++k) {
+        const int it = n * kBlocks + k, s = it % kStages, round = it / kStages;
+        if (round > 0 && !warp_wait(&m.empty[s], (round - 1) & 1)) return;
+        const uint32_t dst = ptx::smem_u32(ring + s * kStageBytes) + 32 * w * 128;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = 4 * j + sub;
+          cp_async16(dst + r * 128 + ((chunk ^ (r & 7)) << 4), src[j] + k * (kBlockCh * 2));
+        }
+        cp_async_arrive(&m.full[s]);
+      }
     }
-    m = block_reduce(m, true, buf);
-    if (m == -CUDART_INF_F) m = 0.0f;
-    float sum = 0.0f;
-    for (int p = tid; p < P; p += 256) sum += s[p] = exp2f(s[p] - m);
-    sum = block_reduce(sum, false, buf);
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    for (int p = tid; p < P; p += 256) mass[p] = fmaf(s[p], inv, mass[p]);
+  };
+
+  auto issue = [&](int n0, int n1) {
+    constexpr uint32_t idesc = ptx::idesc_bf16_f32(kScoreHeads, kTile, 0, 0);
+    for (int n = n0; n < n1; ++n) {
+      const int buf = n % kHeld;
+      bool ok = n < kHeld || ptx::mbar_wait(&m.t_empty[buf], (n / kHeld - 1) & 1, abort_flag, kWaitLimitNs);
+      for (int k = 0; ok && k < kBlocks; ++k) {
+        const int it = n * kBlocks + k, s = it % kStages, acc = k / kAccBlocks;
+        if (k == kAccBlocks && n > 0) ok = ptx::mbar_wait(&m.scratch_empty, (n - 1) & 1, abort_flag, kWaitLimitNs);
+        ok = ok && ptx::mbar_wait(&m.full[s], (it / kStages) & 1, abort_flag, kWaitLimitNs) &&
+             (n > 0 || ptx::mbar_wait(&m.q_full[k], 0, abort_flag, kWaitLimitNs));
+        if (!ok) break;
+        ptx::fence_proxy_async_smem();  // the copies were generic-proxy writes, seen through the barrier
+        ptx::tc_fence_after();
+        const uint64_t dq = smem_desc_sw128(ptx::smem_u32(qbuf + k * kQBlock));
+        const uint64_t dp = smem_desc_sw128(ptx::smem_u32(ring + s * kStageBytes));
+        const uint32_t d = tmem + (acc == 0 ? buf * kTile : kScratchCol + (acc - 1) * kTile);
+#pragma unroll
+        for (int j = 0; j < kBlockCh / 16; ++j)  // 32 B of each row a step
+          ptx::mma_ss(d, dq + 2 * j, dp + 2 * j, idesc, (k % kAccBlocks | j) != 0);
+        ptx::mma_commit(&m.empty[s]);
+      }
+      if (!ok) {
+        give_up();
+        return;
+      }
+      ptx::mma_commit(&m.t_full[buf]);
+    }
+  };
+
+  const int quad = warp & 3, group = (warp >> 2) & 3;  // 32 heads and 32 pages of a tile
+  const bool heads = 32 * quad < a.H;                  // the warp has any
+  const uint32_t my_cols = tmem + (static_cast<uint32_t>(quad) << 21) + 32 * group;
+  float top = -CUDART_INF_F, sum = 0.0f;  // this lane's head over the warp's pages
+  uint32_t ok0 = 0, ok1 = 0;              // of the two held tiles: which of the warp's pages count
+
+  // 16 columns of a tile's logits (unscaled): the three accumulators' sum.
+  auto add_up = [&](int buf, int c, float (&v)[16]) {
+    uint32_t r[2][16];
+    ptx::tmem_ld16(my_cols + buf * kTile + c, r[0]);
+    ptx::tmem_ld16(my_cols + kScratchCol + c, r[1]);
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[0][k]) + __uint_as_float(r[1][k]);
+    ptx::tmem_ld16(my_cols + kScratchCol + kTile + c, r[0]);
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] += __uint_as_float(r[0][k]);
+  };
+  auto pages_ok = [&](int n) {
+    const int p = tile_of(n) * kTile + 32 * group + lane;
+    const bool ok = page_of(p) >= 0;
+    if (p < P && !ok) record_error(a.status, MLA_ERR_INVALID_ARG);
+    return __ballot_sync(0xffffffffu, ok);
+  };
+  auto release = [&](uint64_t* bar) {
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bar);
+  };
+
+  // ---- first sweep: logits and statistics ----
+  if (warp < kSoftWarps) {
+    for (int n = 0; n < mine; ++n) {
+      const int buf = n % kHeld;
+      const uint32_t ok = pages_ok(n);
+      if (n == 0) ok0 = ok;
+      if (n == 1) ok1 = ok;
+      if (!warp_wait(&m.t_full[buf], (n / kHeld) & 1)) break;
+      ptx::tc_fence_after();
+      if (heads) {
+#pragma unroll
+        for (int c = 0; c < 32; c += 16) {
+          float v[16];
+          add_up(buf, c, v);
+          if (!twice) ptx::tmem_st16(my_cols + buf * kTile + c, v);
+          float up = top;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            v[k] = (ok >> (c + k)) & 1 ? v[k] * a.scale_log2 : -CUDART_INF_F;
+            up = fmaxf(up, v[k]);
+          }
+          const float ref = up == -CUDART_INF_F ? 0.0f : up;
+          float s0 = sum * exp2_approx(top - ref), s1 = 0.0f;
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            s0 += exp2_approx(v[k] - ref);
+            s1 += exp2_approx(v[k + 1] - ref);
+          }
+          sum = s0 + s1;
+          top = up;
+        }
+        if (!twice) ptx::tmem_st_wait();
+      }
+      if (twice) release(&m.t_empty[buf]);
+      release(&m.scratch_empty);
+    }
+    m.part[group][32 * quad + lane] = make_float2(top, sum);
+  } else if (warp < kSoftWarps + kCopyWarps) {
+    if (tid == kSoftThreads && mine > 0) {
+      for (int k = 0; k < kBlocks; ++k) {  // rows past the heads keep what they hold: their lanes are not read
+        ptx::mbar_arrive_expect_tx(&m.q_full[k], a.H * kBlockCh * 2);
+        tma_load_2d(qbuf + k * kQBlock, k < 8 ? &maps.q_c : &maps.q_r, k < 8 ? k * kBlockCh : 0, unit * a.H,
+                    &m.q_full[k]);
+      }
+    }
+    __syncwarp();
+    if (mine > 0) produce(0, mine);
+  } else if (lane == 0) {
+    issue(0, mine);
   }
+  ptx::tc_fence_before();
   __syncthreads();
-  float* out = a.scores + (static_cast<size_t>(b) * a.s_q + i) * a.width;
-  for (int p = tid; p < a.width; p += 256) {
-    const bool ok = p < P && lookup_page(a.table, a.max_pages, a.num_pages, b, p * kPage) >= 0;
-    out[p] = ok ? mass[p] : -CUDART_INF_F;
+  ptx::tc_fence_after();
+  ptx::griddep_launch_dependents();
+  for (int h = tid; h < a.H; h += kThreads) {
+    float t = -CUDART_INF_F, l = 0.0f;
+    for (int g = 0; g < 4; ++g) fold(t, l, m.part[g][h].x, m.part[g][h].y);
+    m.cta[h] = make_float2(t, l);
   }
+  __syncwarp();
+  ptx::cluster_sync();
+  const int h = 32 * quad + lane;
+  float inv = 0.0f;
+  if (warp < kSoftWarps && h < a.H) {  // this lane's head over all of the query's pages
+    const uint32_t at = ptx::smem_u32(&m.cta[h]);
+    top = -CUDART_INF_F;
+    sum = 0.0f;
+    for (int r = 0; r < C; ++r) {
+      const float2 v = ld_cluster_f2(ptx::mapa(at, r));
+      fold(top, sum, v.x, v.y);
+    }
+    if (sum > 0.0f) inv = 1.0f / sum;
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // done with the others' memory
+
+  // ---- second sweep: weights and their sum over the heads ----
+  if (warp < kSoftWarps) {
+    float* out = a.scores + static_cast<size_t>(unit) * a.width;
+    const int all = (a.width + kTile - 1) / kTile;
+    for (int n = 0; rank + n * C < all; ++n) {
+      const int p = (rank + n * C) * kTile + 32 * group + lane;
+      uint32_t ok = 0;
+      if (n < mine) {
+        const int k = twice ? mine + n : n, buf = k % kHeld;
+        ok = twice ? pages_ok(k) : n == 0 ? ok0 : ok1;
+        // (after a wait that ran out the loop goes on without the tiles, so that no warp misses a barrier)
+        const bool have = !twice || warp_wait(&m.t_full[buf], (k / kHeld) & 1);
+        ptx::tc_fence_after();
+        if (heads && have) {
+          float v[32];
+#pragma unroll
+          for (int c = 0; c < 32; c += 16) {
+            float u[16];
+            if (twice) {
+              add_up(buf, c, u);
+            } else {
+              uint32_t r[16];
+              ptx::tmem_ld16(my_cols + buf * kTile + c, r);
+              ptx::tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) u[e] = __uint_as_float(r[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              v[c + e] = h < a.H ? exp2_approx(fmaf(u[e], a.scale_log2, -top)) * inv : 0.0f;
+          }
+          m.mass[n & 1][quad][32 * group + lane] = sum_columns(v, lane);
+        }
+        if (twice) {
+          release(&m.t_empty[buf]);
+          release(&m.scratch_empty);
+        }
+        soft_sync();
+      }
+      if (quad == 0 && p < a.width) {
+        float total = -CUDART_INF_F;
+        if ((ok >> lane) & 1) {
+          total = m.mass[n & 1][0][32 * group + lane];
+          for (int q = 1; 32 * q < a.H; ++q) total += m.mass[n & 1][q][32 * group + lane];
+        }
+        out[p] = total;
+      }
+    }
+  } else if (twice && warp < kSoftWarps + kCopyWarps) {
+    produce(mine, 2 * mine);
+  } else if (twice && lane == 0) {
+    issue(mine, 2 * mine);
+  }
+  if (a.num_pages == 0 && P > 0 && tid == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kSoftWarps + kCopyWarps) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTmemCols);
+  }
+  if (tid == 0 && *abort_flag) {  // copies and MMAs in flight get time to end before the memory is given back
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (ptx::globaltimer_ns() - t0 < 100000ull) {
+    }
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // no CTA leaves while its statistics may be read
+}
+
+// ---------------------------------------------------------------- host side
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
+
+// Rows of `width` bf16 channels, in boxes of 64 channels x `rows`, 128-byte swizzle.
+bool make_rows_map(CUtensorMap* m, const void* base, int width, int64_t n, int rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(n)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(width) * 2};
+  const cuuint32_t box[2] = {kBlockCh, static_cast<cuuint32_t>(rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
 cudaError_t launch_page_scores(const PageScoresLaunch& L) {
-  ScoreArgs a{static_cast<const __nv_bfloat16*>(L.digests), L.table, L.seq_lens,
-              static_cast<const __nv_bfloat16*>(L.q_c), static_cast<const __nv_bfloat16*>(L.q_r), L.scores, L.status,
-              L.num_pages, L.max_pages, L.max_seq_len, L.s_q, L.H, L.width, L.scale * kLog2e};
-  const size_t smem = 2 * sizeof(float) * static_cast<size_t>(L.width);
-  if (smem > 200 * 1024) return cudaErrorNotSupported;
-  const cudaError_t e = cudaFuncSetAttribute(page_scores_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  return launch_dependent(page_scores_kernel, dim3(L.s_q, L.B), dim3(256), smem, L.stream, a);
+  const ScoreArgs a{static_cast<const __nv_bfloat16*>(L.digests), L.table, L.seq_lens, L.scores, L.status, L.num_pages,
+                    L.max_pages, L.max_seq_len, L.s_q, L.H, L.width, L.scale * kLog2e};
+  const int64_t units = static_cast<int64_t>(L.B) * L.s_q;
+  Maps maps;
+  const int64_t rows = units * L.H;
+  if (!make_rows_map(&maps.q_c, L.q_c, kDc, rows, L.H) || !make_rows_map(&maps.q_r, L.q_r, kDr, rows, L.H))
+    return cudaErrorInvalidValue;
+  // CTAs a query: those that finish soonest, in units of a tile's time; the query
+  // operand is loaded once a CTA, and set-up and the statistics' exchange cost about half a tile
+  const int tiles = (L.width + kTile - 1) / kTile;
+  int best = 1;
+  double best_cost = 1e30;
+  for (int c = 1; c <= 8; c *= 2) {
+    const int per = (tiles + c - 1) / c;
+    const int64_t waves = (units * c + sms - 1) / sms;
+    const double cost = waves * (per * (per > kHeld ? 2.0 : 1.0) + L.H / 128.0 + 0.5);
+    if (cost < best_cost * 0.97) {
+      best_cost = cost;
+      best = c;
+    }
+  }
+  e = cudaFuncSetAttribute(page_scores_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(units * best));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = L.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(best), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, page_scores_kernel, a, maps);
 }
 
 }  // namespace mla
