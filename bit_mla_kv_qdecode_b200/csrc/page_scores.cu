@@ -25,16 +25,18 @@
 // heads come with nine tiled loads and stay for all tiles. (TMA's gather of four
 // rows a request moved 10 GB/s an SM at 128 bytes a row, these copies 43.)
 // Warp roles:
-//   warps 0-15   a quarter of the heads and a quarter of a tile's pages each:
-//                statistics, later weights and their sum over the heads
-//   warps 16-19  copies
-//   warp 20      tensor memory, MMA issue
+//   warps 0-7   a quarter of the heads and half of a tile's pages each:
+//               statistics, later weights and their sum over the heads
+//   warps 8-15  copies (four warps reached 42 GB/s, eight 70)
+//   warps 16-18 MMA issue, one accumulator each (a stage costs its issuing
+//               thread 380 ns of waits and issue, its MMAs 130); tensor memory
 // The CTAs' statistics meet in distributed shared memory, in rank order, so
 // results do not depend on timing. Every wait is bounded; one that runs out
 // sets MLA_ERR_TIMEOUT and leaves the scores undefined.
 #include <cuda.h>
 #include <math_constants.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "mla_common.cuh"
@@ -44,17 +46,17 @@
 namespace mla {
 namespace {
 
-constexpr int kSoftWarps = 16, kCopyWarps = 4;
+constexpr int kSoftWarps = 8, kCopyWarps = 8;
 constexpr int kSoftThreads = kSoftWarps * 32;
-constexpr int kThreads = (kSoftWarps + kCopyWarps + 1) * 32;
+constexpr int kMaxCluster = 8;
+constexpr int kAccs = 3;                           // accumulators of a logit, a warp that issues for each
+constexpr int kMmaWarp = kSoftWarps + kCopyWarps;  // the first of them
+constexpr int kThreads = (kMmaWarp + kAccs) * 32;
 constexpr int kTile = 128;                         // pages of a tile
 constexpr int kBlockCh = 64;                       // channels of one operand stage (128 B a row)
 constexpr int kBlocks = kDqk / kBlockCh;           // 9: eight of the content, one of the RoPE part
 constexpr int kStageBytes = kTile * kBlockCh * 2;  // 16 KB
-constexpr int kQBlock = kScoreHeads * kBlockCh * 2;
-constexpr int kStages = 4;
-constexpr int kAccs = 3;                           // accumulators of a logit
-constexpr int kAccBlocks = kBlocks / kAccs;
+constexpr int kMaxStages = 12;
 constexpr int kHeld = 2;                           // tiles whose logits tensor memory holds
 constexpr uint32_t kScratchCol = kHeld * kTile;
 constexpr uint32_t kTmemCols = 512;
@@ -69,6 +71,7 @@ struct ScoreArgs {
   float* scores;
   int* status;
   int num_pages, max_pages, max_seq_len, s_q, H, width;
+  int q_block, stages;  // bytes of a query block in shared memory; operand stages of the ring
   float scale_log2;
 };
 
@@ -78,16 +81,20 @@ struct Maps {
 };
 
 struct Misc {
-  uint64_t full[kStages], empty[kStages], q_full[kBlocks], t_full[kHeld], t_empty[kHeld], scratch_empty;
-  float2 part[4][kScoreHeads];  // (maximum, sum) of each head over a quarter of the CTA's pages
-  float2 cta[kScoreHeads];      // over the CTA's pages
+  uint64_t full[kMaxStages], empty[kMaxStages], q_full[kBlocks], t_full[kHeld], t_empty[kHeld], scratch_empty;
+  float2 half[kScoreHeads];               // (maximum, sum) of each head over one half of the CTA's pages
+  float2 part[kMaxCluster][kScoreHeads];  // over each CTA's pages, written by the CTAs
   float mass[2][4][kTile];      // a tile's weights, summed over a quarter of the heads
+  uint32_t ok[2][kTile / 32];   // a tile's pages that count
   uint32_t tmem;
   int abort;
 };
-constexpr int kSmemBytes = kStages * kStageBytes + kBlocks * kQBlock + static_cast<int>(sizeof(Misc)) + 1024;
-static_assert(kSmemBytes <= kSmemLimit, "shared memory budget");
-static_assert(kSmemBytes > kSmemLimit / 2, "one CTA per SM keeps the 512-column TMEM allocation uncontended");
+// Shared memory: query blocks, ring, Misc. A query block holds the heads there
+// are, in whole groups of eight rows; the MMA reads 128 rows, those past the heads
+// from whatever follows (their lanes are not used), which the ring's size covers.
+constexpr int kMinStages = 4;
+constexpr int kSmemFixed = static_cast<int>(sizeof(Misc)) + 1024;
+static_assert(kBlocks * kScoreHeads * 128 + kMinStages * kStageBytes + kSmemFixed <= kSmemLimit, "shared memory budget");
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -106,10 +113,8 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* tmap, int x, 
       : "memory");
 }
 
-__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster_f2(uint32_t addr, float2 v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
 }
 
 // K-major operand of 128-byte rows in the 128-byte swizzle: 8-row groups 1,024 B apart.
@@ -134,10 +139,10 @@ __device__ __forceinline__ void fold(float& m, float& l, float top, float sum) {
   m = up;
 }
 
-// Sum each of 32 columns over the warp's lanes; lane l returns column l's.
-__device__ __forceinline__ float sum_columns(float (&v)[32], int lane) {
+// Sum each of 16 columns over the warp's lanes; lane l returns column l & 15's.
+__device__ __forceinline__ float sum_columns(float (&v)[16], int lane) {
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) {
+  for (int s = 8; s > 0; s >>= 1) {
     const bool up = lane & s;
 #pragma unroll
     for (int k = 0; k < s; ++k) {
@@ -145,15 +150,17 @@ __device__ __forceinline__ float sum_columns(float (&v)[32], int lane) {
       v[k] = keep + __shfl_xor_sync(0xffffffffu, give, s);
     }
   }
-  return v[0];
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 
+// kTwice: a CTA may have more tiles than it can hold, and goes over them twice.
+template <bool kTwice>
 __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArgs a, const __grid_constant__ Maps maps) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (ptx::smem_u32(smem_raw) & 1023)) & 1023);
-  uint8_t* ring = smem;
-  uint8_t* qbuf = ring + kStages * kStageBytes;
-  Misc& m = *reinterpret_cast<Misc*>(qbuf + kBlocks * kQBlock);
+  uint8_t* qbuf = smem;
+  uint8_t* ring = qbuf + kBlocks * a.q_block;
+  Misc& m = *reinterpret_cast<Misc*>(ring + a.stages * kStageBytes);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(ptx::cluster_ctarank());
   int C;
@@ -161,20 +168,20 @@ __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArg
   const int unit = blockIdx.x / C, b = unit / a.s_q, i = unit - b * a.s_q;
 
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < a.stages; ++s) {
       ptx::mbar_init(&m.full[s], kCopyWarps * 32);
       ptx::mbar_init(&m.empty[s], 1);
     }
     for (int k = 0; k < kBlocks; ++k) ptx::mbar_init(&m.q_full[k], 1);
     for (int t = 0; t < kHeld; ++t) {
-      ptx::mbar_init(&m.t_full[t], 1);
+      ptx::mbar_init(&m.t_full[t], kAccs);
       ptx::mbar_init(&m.t_empty[t], kSoftWarps);
     }
     ptx::mbar_init(&m.scratch_empty, kSoftWarps);
     m.abort = 0;
     ptx::fence_mbar_init_cluster();
   }
-  if (warp == kSoftWarps + kCopyWarps) {
+  if (warp == kMmaWarp) {
     ptx::tmem_alloc(&m.tmem, kTmemCols);
     ptx::tmem_relinquish();
   }
@@ -184,10 +191,16 @@ __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArg
   }
   ptx::tc_fence_before();
   __syncthreads();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // waited for before the first remote store
   ptx::tc_fence_after();
   const uint32_t tmem = m.tmem;
   ptx::griddep_wait();
 
+  // the copying warps' first table entries come along with the length
+  const int copy_page = 16 * (warp - kSoftWarps) + (lane & 15);  // of a tile: the page this lane looks up
+  auto table_at = [&](int p) { return p < a.max_pages ? __ldg(a.table + static_cast<size_t>(b) * a.max_pages + p) : -1; };
+  int entry = -1;
+  if (warp >= kSoftWarps && warp < kMmaWarp) entry = table_at(rank * kTile + copy_page);
   int T = __ldg(a.seq_lens + b);
   if (T < 0 || T > a.max_seq_len) {
     if (tid == 0 && rank == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
@@ -196,7 +209,6 @@ __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArg
   const int L = T - a.s_q + 1 + i, P = L > 0 ? (L - 1) / kPage : 0;
   const int tiles = (P + kTile - 1) / kTile;
   const int mine = a.num_pages > 0 && tiles > rank ? (tiles - 1 - rank) / C + 1 : 0;
-  const bool twice = mine > kHeld;
   volatile int* abort_flag = &m.abort;
   auto give_up = [&] {
     *abort_flag = 1;
@@ -208,33 +220,31 @@ __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArg
     if (!ok) give_up();
     return ok;
   };
-  auto page_of = [&](int p) -> int {
-    return p < P ? lookup_page(a.table, a.max_pages, a.num_pages, b, p * kPage) : -1;
-  };
+  auto page_ok = [&](int p) { return p < P && page_valid(table_at(p), a.num_pages); };
   auto tile_of = [&](int n) { return rank + (n < mine ? n : n - mine) * C; };  // n counts over both sweeps
 
   // Copy the digests of this CTA's tiles into the ring. Eight lanes take one
-  // page's 128 bytes of a stage, a warp 32 pages.
+  // page's 128 bytes of a stage, a warp 16 pages. `entry` is the lane's table
+  // entry of the next tile.
   auto produce = [&](int n0, int n1) {
     const int w = warp - kSoftWarps, sub = lane >> 3, chunk = lane & 7;
-    auto lane_page = [&](int n) {  // pages that are none read page 0; their logits are masked
-      return n < n1 ? max(page_of(tile_of(n) * kTile + 32 * w + lane), 0) : 0;
-    };
-    int next = lane_page(n0);
     for (int n = n0; n < n1; ++n) {
-      const uint8_t* src[8];
+      // pages that are none read page 0; their logits are masked
+      const bool ok = tile_of(n) * kTile + copy_page < P && page_valid(entry, a.num_pages);
+      const int mine_page = ok ? entry : 0;
+      const uint8_t* src[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int page = __shfl_sync(0xffffffffu, next, 4 * j + sub);
+      for (int j = 0; j < 4; ++j) {
+        const int page = __shfl_sync(0xffffffffu, mine_page, 4 * j + sub);
         src[j] = reinterpret_cast<const uint8_t*>(a.digests + static_cast<size_t>(page) * kDqk) + 16 * chunk;
       }
-      next = lane_page(n + 1);
+      if (n + 1 < 2 * mine) entry = table_at(tile_of(n + 1) * kTile + copy_page);
       for (int k = 0; k < kBlocks; ++k) {
-        const int it = n * kBlocks + k, s = it % kStages, round = it / kStages;
+        const int it = n * kBlocks + k, round = it / a.stages, s = it - round * a.stages;
         if (round > 0 && !warp_wait(&m.empty[s], (round - 1) & 1)) return;
-        const uint32_t dst = ptx::smem_u32(ring + s * kStageBytes) + 32 * w * 128;
+        const uint32_t dst = ptx::smem_u32(ring + s * kStageBytes) + 16 * w * 128;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           const int r = 4 * j + sub;
           cp_async16(dst + r * 128 + ((chunk ^ (r & 7)) << 4), src[j] + k * (kBlockCh * 2));
         }
@@ -243,25 +253,28 @@ __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArg
     }
   };
 
+  // Accumulator e takes channel blocks e, e + 3 and e + 6.
   auto issue = [&](int n0, int n1) {
     constexpr uint32_t idesc = ptx::idesc_bf16_f32(kScoreHeads, kTile, 0, 0);
+    const int e = warp - kMmaWarp;
     for (int n = n0; n < n1; ++n) {
       const int buf = n % kHeld;
-      bool ok = n < kHeld || ptx::mbar_wait(&m.t_empty[buf], (n / kHeld - 1) & 1, abort_flag, kWaitLimitNs);
-      for (int k = 0; ok && k < kBlocks; ++k) {
-        const int it = n * kBlocks + k, s = it % kStages, acc = k / kAccBlocks;
-        if (k == kAccBlocks && n > 0) ok = ptx::mbar_wait(&m.scratch_empty, (n - 1) & 1, abort_flag, kWaitLimitNs);
-        ok = ok && ptx::mbar_wait(&m.full[s], (it / kStages) & 1, abort_flag, kWaitLimitNs) &&
+      const uint32_t d = tmem + (e == 0 ? buf * kTile : kScratchCol + (e - 1) * kTile);
+      bool ok = true;
+      if (e == 0 && n >= kHeld) ok = ptx::mbar_wait(&m.t_empty[buf], (n / kHeld - 1) & 1, abort_flag, kWaitLimitNs);
+      if (e > 0 && n > 0) ok = ptx::mbar_wait(&m.scratch_empty, (n - 1) & 1, abort_flag, kWaitLimitNs);
+      for (int k = e; ok && k < kBlocks; k += kAccs) {
+        const int it = n * kBlocks + k, round = it / a.stages, s = it - round * a.stages;
+        ok = ptx::mbar_wait(&m.full[s], round & 1, abort_flag, kWaitLimitNs) &&
              (n > 0 || ptx::mbar_wait(&m.q_full[k], 0, abort_flag, kWaitLimitNs));
         if (!ok) break;
         ptx::fence_proxy_async_smem();  // the copies were generic-proxy writes, seen through the barrier
         ptx::tc_fence_after();
-        const uint64_t dq = smem_desc_sw128(ptx::smem_u32(qbuf + k * kQBlock));
+        const uint64_t dq = smem_desc_sw128(ptx::smem_u32(qbuf + k * a.q_block));
         const uint64_t dp = smem_desc_sw128(ptx::smem_u32(ring + s * kStageBytes));
-        const uint32_t d = tmem + (acc == 0 ? buf * kTile : kScratchCol + (acc - 1) * kTile);
 #pragma unroll
         for (int j = 0; j < kBlockCh / 16; ++j)  // 32 B of each row a step
-          ptx::mma_ss(d, dq + 2 * j, dp + 2 * j, idesc, (k % kAccBlocks | j) != 0);
+          ptx::mma_ss(d, dq + 2 * j, dp + 2 * j, idesc, (k != e) | (j != 0));
         ptx::mma_commit(&m.empty[s]);
       }
       if (!ok) {
@@ -272,28 +285,27 @@ __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArg
     }
   };
 
-  const int quad = warp & 3, group = (warp >> 2) & 3;  // 32 heads and 32 pages of a tile
+  const int quad = warp & 3, group = (warp >> 2) & 1;  // 32 heads and 64 pages of a tile
   const bool heads = 32 * quad < a.H;                  // the warp has any
-  const uint32_t my_cols = tmem + (static_cast<uint32_t>(quad) << 21) + 32 * group;
+  const uint32_t my_cols = tmem + (static_cast<uint32_t>(quad) << 21) + 64 * group;
   float top = -CUDART_INF_F, sum = 0.0f;  // this lane's head over the warp's pages
-  uint32_t ok0 = 0, ok1 = 0;              // of the two held tiles: which of the warp's pages count
+  float refs[kHeld][4] = {};              // of the held tiles: what each 16 columns' exponents are relative to
 
-  // 16 columns of a tile's logits (unscaled): the three accumulators' sum.
+  // 16 columns of a tile's logits, in powers of two: the three accumulators' sum, scaled.
   auto add_up = [&](int buf, int c, float (&v)[16]) {
-    uint32_t r[2][16];
+    uint32_t r[kAccs][16];
     ptx::tmem_ld16(my_cols + buf * kTile + c, r[0]);
     ptx::tmem_ld16(my_cols + kScratchCol + c, r[1]);
+    ptx::tmem_ld16(my_cols + kScratchCol + kTile + c, r[2]);
     ptx::tmem_ld_wait();
 #pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[0][k]) + __uint_as_float(r[1][k]);
-    ptx::tmem_ld16(my_cols + kScratchCol + kTile + c, r[0]);
-    ptx::tmem_ld_wait();
-#pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] += __uint_as_float(r[0][k]);
+    for (int k = 0; k < 16; ++k)
+      v[k] = (__uint_as_float(r[0][k]) + __uint_as_float(r[1][k]) + __uint_as_float(r[2][k])) * a.scale_log2;
   };
-  auto pages_ok = [&](int n) {
-    const int p = tile_of(n) * kTile + 32 * group + lane;
-    const bool ok = page_of(p) >= 0;
+  // Which of 32 pages of tile n count; bad table entries are flagged.
+  auto pages_ok = [&](int n, int half) {
+    const int p = tile_of(n) * kTile + 64 * group + 32 * half + lane;
+    const bool ok = page_ok(p);
     if (p < P && !ok) record_error(a.status, MLA_ERR_INVALID_ARG);
     return __ballot_sync(0xffffffffu, ok);
   };
@@ -307,44 +319,54 @@ __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArg
   if (warp < kSoftWarps) {
     for (int n = 0; n < mine; ++n) {
       const int buf = n % kHeld;
-      const uint32_t ok = pages_ok(n);
-      if (n == 0) ok0 = ok;
-      if (n == 1) ok1 = ok;
+      const uint32_t ok0 = pages_ok(n, 0), ok1 = pages_ok(n, 1);
+      if (!kTwice && quad == 0 && lane < 2) m.ok[n][2 * group + lane] = lane == 0 ? ok0 : ok1;
       if (!warp_wait(&m.t_full[buf], (n / kHeld) & 1)) break;
       ptx::tc_fence_after();
       if (heads) {
 #pragma unroll
-        for (int c = 0; c < 32; c += 16) {
+        for (int q = 0; q < 4; ++q) {
+          const int c = 16 * q;
           float v[16];
           add_up(buf, c, v);
-          if (!twice) ptx::tmem_st16(my_cols + buf * kTile + c, v);
+          const uint32_t mask = (q < 2 ? ok0 : ok1) >> (c & 16) & 0xffffu;
+          if (mask != 0xffffu) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = (mask >> k) & 1 ? v[k] : -CUDART_INF_F;
+          }
           float up = top;
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            v[k] = (ok >> (c + k)) & 1 ? v[k] * a.scale_log2 : -CUDART_INF_F;
-            up = fmaxf(up, v[k]);
-          }
+          for (int k = 0; k < 16; ++k) up = fmaxf(up, v[k]);
           const float ref = up == -CUDART_INF_F ? 0.0f : up;
           float s0 = sum * exp2_approx(top - ref), s1 = 0.0f;
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {
-            s0 += exp2_approx(v[k] - ref);
-            s1 += exp2_approx(v[k + 1] - ref);
+            s0 += v[k] = exp2_approx(v[k] - ref);
+            s1 += v[k + 1] = exp2_approx(v[k + 1] - ref);
+          }
+          if (!kTwice) {
+            ptx::tmem_st16(my_cols + buf * kTile + c, v);
+            if (n == 0) refs[0][q] = ref;
+            if (n == 1) refs[1][q] = ref;
           }
           sum = s0 + s1;
           top = up;
         }
-        if (!twice) ptx::tmem_st_wait();
+        if (!kTwice) ptx::tmem_st_wait();
       }
-      if (twice) release(&m.t_empty[buf]);
+      if (kTwice) release(&m.t_empty[buf]);
       release(&m.scratch_empty);
     }
-    m.part[group][32 * quad + lane] = make_float2(top, sum);
-  } else if (warp < kSoftWarps + kCopyWarps) {
+    // the halves' statistics, then every CTA's in every CTA's memory
+    const int h = 32 * quad + lane;
+    if (group == 1) m.half[h] = make_float2(top, sum);
+    soft_sync();
+    if (group == 0) fold(top, sum, m.half[h].x, m.half[h].y);
+    } else if (warp < kMmaWarp) {
     if (tid == kSoftThreads && mine > 0) {
       for (int k = 0; k < kBlocks; ++k) {  // rows past the heads keep what they hold: their lanes are not read
         ptx::mbar_arrive_expect_tx(&m.q_full[k], a.H * kBlockCh * 2);
-        tma_load_2d(qbuf + k * kQBlock, k < 8 ? &maps.q_c : &maps.q_r, k < 8 ? k * kBlockCh : 0, unit * a.H,
+        tma_load_2d(qbuf + k * a.q_block, k < 8 ? &maps.q_c : &maps.q_r, k < 8 ? k * kBlockCh : 0, unit * a.H,
                     &m.q_full[k]);
       }
     }
@@ -353,90 +375,93 @@ __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArg
   } else if (lane == 0) {
     issue(0, mine);
   }
-  ptx::tc_fence_before();
-  __syncthreads();
-  ptx::tc_fence_after();
   ptx::griddep_launch_dependents();
-  for (int h = tid; h < a.H; h += kThreads) {
-    float t = -CUDART_INF_F, l = 0.0f;
-    for (int g = 0; g < 4; ++g) fold(t, l, m.part[g][h].x, m.part[g][h].y);
-    m.cta[h] = make_float2(t, l);
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA runs
+  const int h = 32 * quad + lane;
+  if (warp < 4 && h < a.H) {
+    const uint32_t at = ptx::smem_u32(&m.part[rank][h]);
+    for (int r = 0; r < C; ++r) st_cluster_f2(ptx::mapa(at, r), make_float2(top, sum));
   }
+  ptx::tc_fence_before();
   __syncwarp();
   ptx::cluster_sync();
-  const int h = 32 * quad + lane;
+  ptx::tc_fence_after();
   float inv = 0.0f;
   if (warp < kSoftWarps && h < a.H) {  // this lane's head over all of the query's pages
-    const uint32_t at = ptx::smem_u32(&m.cta[h]);
     top = -CUDART_INF_F;
+    for (int r = 0; r < C; ++r) top = fmaxf(top, m.part[r][h].x);
+    if (top == -CUDART_INF_F) top = 0.0f;
     sum = 0.0f;
-    for (int r = 0; r < C; ++r) {
-      const float2 v = ld_cluster_f2(ptx::mapa(at, r));
-      fold(top, sum, v.x, v.y);
-    }
+    for (int r = 0; r < C; ++r) sum = fmaf(m.part[r][h].y, exp2_approx(m.part[r][h].x - top), sum);
     if (sum > 0.0f) inv = 1.0f / sum;
   }
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // done with the others' memory
 
   // ---- second sweep: weights and their sum over the heads ----
   if (warp < kSoftWarps) {
     float* out = a.scores + static_cast<size_t>(unit) * a.width;
     const int all = (a.width + kTile - 1) / kTile;
     for (int n = 0; rank + n * C < all; ++n) {
-      const int p = (rank + n * C) * kTile + 32 * group + lane;
-      uint32_t ok = 0;
       if (n < mine) {
-        const int k = twice ? mine + n : n, buf = k % kHeld;
-        ok = twice ? pages_ok(k) : n == 0 ? ok0 : ok1;
-        // (after a wait that ran out the loop goes on without the tiles, so that no warp misses a barrier)
-        const bool have = !twice || warp_wait(&m.t_full[buf], (k / kHeld) & 1);
-        ptx::tc_fence_after();
+        const int k = kTwice ? mine + n : n, buf = k % kHeld;
+        bool have = true;
+        if (kTwice) {
+          const uint32_t ok0 = pages_ok(k, 0), ok1 = pages_ok(k, 1);
+          if (quad == 0 && lane < 2) m.ok[n & 1][2 * group + lane] = lane == 0 ? ok0 : ok1;
+          // (after a wait that ran out the loop goes on without the tiles, so that no warp misses a barrier)
+          have = warp_wait(&m.t_full[buf], (k / kHeld) & 1);
+          ptx::tc_fence_after();
+        }
         if (heads && have) {
-          float v[32];
 #pragma unroll
-          for (int c = 0; c < 32; c += 16) {
-            float u[16];
-            if (twice) {
-              add_up(buf, c, u);
+          for (int q = 0; q < 4; ++q) {
+            const int c = 16 * q;
+            float v[16], f;
+            if (kTwice) {
+              add_up(buf, c, v);
+              f = inv;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = exp2_approx(v[e] - top);
             } else {
               uint32_t r[16];
               ptx::tmem_ld16(my_cols + buf * kTile + c, r);
               ptx::tmem_ld_wait();
+              f = exp2_approx((n == 0 ? refs[0][q] : refs[1][q]) - top) * inv;
 #pragma unroll
-              for (int e = 0; e < 16; ++e) u[e] = __uint_as_float(r[e]);
+              for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(r[e]);
             }
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              v[c + e] = h < a.H ? exp2_approx(fmaf(u[e], a.scale_log2, -top)) * inv : 0.0f;
+            for (int e = 0; e < 16; ++e) v[e] = h < a.H ? v[e] * f : 0.0f;
+            const float mass = sum_columns(v, lane);
+            if (lane < 16) m.mass[n & 1][quad][64 * group + c + lane] = mass;
           }
-          m.mass[n & 1][quad][32 * group + lane] = sum_columns(v, lane);
         }
-        if (twice) {
+        if (kTwice) {
           release(&m.t_empty[buf]);
           release(&m.scratch_empty);
         }
         soft_sync();
       }
-      if (quad == 0 && p < a.width) {
+      const int p = (rank + n * C) * kTile + tid;
+      if (tid < kTile && p < a.width) {
         float total = -CUDART_INF_F;
-        if ((ok >> lane) & 1) {
-          total = m.mass[n & 1][0][32 * group + lane];
-          for (int q = 1; 32 * q < a.H; ++q) total += m.mass[n & 1][q][32 * group + lane];
+        if (n < mine && ((m.ok[n & 1][warp] >> lane) & 1)) {
+          total = m.mass[n & 1][0][tid];
+          for (int q = 1; 32 * q < a.H; ++q) total += m.mass[n & 1][q][tid];
         }
         out[p] = total;
       }
     }
-  } else if (twice && warp < kSoftWarps + kCopyWarps) {
+  } else if (kTwice && warp < kMmaWarp) {
     produce(mine, 2 * mine);
-  } else if (twice && lane == 0) {
+  } else if (kTwice && lane == 0) {
     issue(mine, 2 * mine);
   }
   if (a.num_pages == 0 && P > 0 && tid == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
 
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == kSoftWarps + kCopyWarps) {
+  if (warp == kMmaWarp) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);
   }
@@ -445,8 +470,6 @@ __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArg
     while (ptx::globaltimer_ns() - t0 < 100000ull) {
     }
   }
-  __syncwarp();
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // no CTA leaves while its statistics may be read
 }
 
 // ---------------------------------------------------------------- host side
@@ -488,8 +511,11 @@ cudaError_t launch_page_scores(const PageScoresLaunch& L) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
+  const int q_block = (L.H + 7) / 8 * 1024;
+  const int stages = std::min((kSmemLimit - kSmemFixed - kBlocks * q_block) / kStageBytes, kMaxStages);
+  const int smem = kBlocks * q_block + stages * kStageBytes + kSmemFixed;
   const ScoreArgs a{static_cast<const __nv_bfloat16*>(L.digests), L.table, L.seq_lens, L.scores, L.status, L.num_pages,
-                    L.max_pages, L.max_seq_len, L.s_q, L.H, L.width, L.scale * kLog2e};
+                    L.max_pages, L.max_seq_len, L.s_q, L.H, L.width, q_block, stages, L.scale * kLog2e};
   const int64_t units = static_cast<int64_t>(L.B) * L.s_q;
   Maps maps;
   const int64_t rows = units * L.H;
@@ -500,7 +526,7 @@ cudaError_t launch_page_scores(const PageScoresLaunch& L) {
   const int tiles = (L.width + kTile - 1) / kTile;
   int best = 1;
   double best_cost = 1e30;
-  for (int c = 1; c <= 8; c *= 2) {
+  for (int c = 1; c <= kMaxCluster; c *= 2) {
     const int per = (tiles + c - 1) / c;
     const int64_t waves = (units * c + sms - 1) / sms;
     const double cost = waves * (per * (per > kHeld ? 2.0 : 1.0) + L.H / 128.0 + 0.5);
@@ -509,12 +535,13 @@ cudaError_t launch_page_scores(const PageScoresLaunch& L) {
       best = c;
     }
   }
-  e = cudaFuncSetAttribute(page_scores_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  auto kern = (tiles + best - 1) / best > kHeld ? page_scores_kernel<true> : page_scores_kernel<false>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(units * best));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = smem;  // more than half of an SM's: one CTA keeps the 512-column TMEM allocation uncontended
   cfg.stream = L.stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -523,7 +550,7 @@ cudaError_t launch_page_scores(const PageScoresLaunch& L) {
   attr[1].val.clusterDim = {static_cast<unsigned>(best), 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, page_scores_kernel, a, maps);
+  return cudaLaunchKernelEx(&cfg, kern, a, maps);
 }
 
 }  // namespace mla
