@@ -205,26 +205,49 @@ def mla_qdecode_hybrid(desc, pool, block_table, hist_lens, max_hist_len, bf16_po
     return out, lse
 
 
-def _ints(t, name, shape, device):
-    """Address of an optional int32 tensor of the given shape on `device`."""
-    if t is None:
-        return None
-    p = _need(t, name, torch.int32, shape)
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    return p
+def _refuse(t, name, dtype, shape, index):
+    """Raise the error of an argument that does not fit (the contiguity check comes last)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _on(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
+def _arg(t, name, dtype, shape, index):
+    """Address of a dense tensor of this type and shape on CUDA device `index`."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, index)
 
 
-def _empty(shape, dtype, device, stream):
+def _opt(t, name, dtype, shape, index):
+    return None if t is None else _arg(t, name, dtype, shape, index)
+
+
+def _device_index(t, name, dtype, dims):
+    """CUDA device of the tensor that the other arguments have to join, which has `dims` dimensions."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
+    if not t.is_cuda or t.dtype is not dtype:
+        _refuse(t, name, dtype, t.shape, 0)
+    return t.get_device()
+
+
+def _empty(shape, dtype, index, stream):
     """Uninitialised tensor for a kernel on `stream` (None: the current stream): taken from that
     stream's memory, and not given back while the current stream may still read it."""
     if stream is not None:
+        device = torch.device("cuda", index)
         cur = torch.cuda.current_stream(device)
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device) if int(stream) else torch.cuda.default_stream(device)
@@ -233,69 +256,62 @@ def _empty(shape, dtype, device, stream):
                 t = torch.empty(shape, dtype=dtype, device=device)
             t.record_stream(cur)
             return t
-    return torch.empty(shape, dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=index)
 
 
-def _call(name, device, stream, *args):
-    """Run a library call with `device` current, on `stream` or the device's current stream."""
+def _call(name, index, stream, *args):
+    """Run a library call with CUDA device `index` current, on `stream` or that device's current stream."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    s = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
     fn = getattr(_lib.load(), name)
-    if device.index is None or torch.cuda.current_device() == device.index:
-        code = fn(*args, s)
+    if torch.cuda.current_device() == index:
+        code = fn(*args, int(stream))
     else:
-        with torch.cuda.device(device):
-            code = fn(*args, s)
+        with torch.cuda.device(index):
+            code = fn(*args, int(stream))
     if code:
         check(name, code)
 
 
-def _pool(desc, pool):
+def _pool(desc, pool, index):
     """Address of a quantized pool, which must hold every page of desc."""
-    p = _need(pool, "pool", torch.uint8)
+    shape = pool.shape if isinstance(pool, torch.Tensor) else None
+    p = _arg(pool, "pool", torch.uint8, shape, index)
     if pool.numel() < desc.num_pages * mla_qcache_page_bytes(desc):
         raise ValueError("pool is smaller than desc.num_pages pages")
     return p
 
 
-def _table(block_table, B, device):
-    p = _need(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table must have shape ({B}, max_pages), got {tuple(block_table.shape)}")
-    _on(device, block_table=block_table)
-    return p
+def _table(block_table, B, index):
+    """(address, row length) of a block table of B requests."""
+    shape = block_table.shape if isinstance(block_table, torch.Tensor) else (B, 1)
+    if len(shape) != 2 or shape[0] != B:
+        raise ValueError(f"block_table must have shape ({B}, max_pages), got {tuple(shape)}")
+    return _arg(block_table, "block_table", torch.int32, shape, index), shape[1]
 
 
-def _rows(t, name, shape):
+def _rows(t, name, shape, index):
     """(address, row stride) of a bf16 tensor [B, n, ...] whose B * n rows are evenly spaced."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != index:
+        _refuse(t, name, torch.bfloat16, shape, index)
     B, n = shape[0], shape[1]
-    if t.stride(-1) != 1 or (B > 1 and n > 1 and t.stride(0) != n * t.stride(1)):
+    stride = t.stride()
+    if t.numel() and (stride[-1] != 1 or (B > 1 and n > 1 and stride[0] != n * stride[1])):
         raise ValueError(f"{name} must have unit stride in its last dimension and evenly spaced rows")
-    return t.data_ptr(), (t.stride(1) if n > 1 else t.stride(0) if B > 1 else 0)
+    return t.data_ptr(), (stride[1] if n > 1 else stride[0] if B > 1 else 0)
 
 
-def _out_rows(t, name, rows, width):
+def _out_rows(t, name, rows, width, index):
     """(address, row stride) of a bf16 output [rows, width] with unit stride in a row."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != (rows, width):
-        raise ValueError(f"{name} must have shape {(rows, width)}, got {tuple(t.shape)}")
-    if t.stride(1) != 1 or (rows > 1 and t.stride(0) < width):
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.shape != (rows, width) \
+            or t.get_device() != index:
+        _refuse(t, name, torch.bfloat16, (rows, width), index)
+    stride = t.stride()
+    if stride[1] != 1 or (rows > 1 and stride[0] < width):
         raise ValueError(f"{name} must have unit stride in a row and rows that do not overlap")
-    return t.data_ptr(), t.stride(0) if rows > 1 else width
+    return t.data_ptr(), stride[0] if rows > 1 else width
 
 
 _ROPE_PAIRS = {"interleaved": _lib.MLA_ROPE_INTERLEAVED, "half": _lib.MLA_ROPE_HALF}
@@ -308,39 +324,36 @@ def mla_qcache_append_norm_rope(desc, pool, block_table, seq_lens_before, kv, no
     queries, quantize and write. kv [B, n, 576] and q [B, n, H, 64] may be column ranges of wider
     tensors; norm_weight may be None (ones); convention names the rotary pairs as in
     fold.rotary_pairs. Returns q_out [B, n, H, 64] (None without q). See include/mla_qcache.h."""
-    if convention not in _ROPE_PAIRS:
+    pairs = _ROPE_PAIRS.get(convention)
+    if pairs is None:
         raise ValueError(f"unknown rotary convention {convention!r}")
-    if not isinstance(kv, torch.Tensor) or kv.dim() != 3:
-        raise ValueError("kv must be a tensor [B, n, 576]")
+    dev = _device_index(kv, "kv", torch.bfloat16, 3)
     B, n = kv.shape[0], kv.shape[1]
-    dev = kv.device
-    pkv, kv_stride = _rows(kv, "kv", (B, n, D_C + D_R))
+    pkv, kv_stride = _rows(kv, "kv", (B, n, D_C + D_R), dev)
     H, pq, q_token, q_head, pqo = 0, None, 0, 0, None
-    if q is not None and q.dim() != 4:
-        raise ValueError("q must be a tensor [B, n, H, 64]")
-    if q is not None and q.shape[2] > 0:
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 4:
+            raise ValueError("q must be a tensor [B, n, H, 64]")
         H = q.shape[2]
-        pq, q_token = _rows(q, "q", (B, n, H, D_R))
+        pq, q_token = _rows(q, "q", (B, n, H, D_R), dev)
         q_head = q.stride(2) if H > 1 else 0
         if q_out is None:
             q_out = _empty((B, n, H, D_R), torch.bfloat16, dev, stream)
-        pqo = _need(q_out, "q_out", torch.bfloat16, (B, n, H, D_R))
+        pqo = _arg(q_out, "q_out", torch.bfloat16, (B, n, H, D_R), dev)
+        if H == 0:
+            pq = pqo = None
     elif q_out is not None:
-        if q is None:
-            raise ValueError("q_out needs q")
-        _need(q_out, "q_out", torch.bfloat16, (B, n, 0, D_R))
-    elif q is not None:
-        q_out = _empty((B, n, 0, D_R), torch.bfloat16, dev, stream)
-    pw = None if norm_weight is None else _need(norm_weight, "norm_weight", torch.bfloat16, (D_C,))
-    pcs = _need(cos_sin, "cos_sin", torch.float32)
-    if cos_sin.dim() != 2 or cos_sin.shape[1] != D_R:
-        raise ValueError(f"cos_sin must have shape (positions, {D_R}), got {tuple(cos_sin.shape)}")
-    prows = None if rows_out is None else _need(rows_out, "rows_out", torch.bfloat16, (B, n, D_C + D_R))
-    _on(dev, pool=pool, norm_weight=norm_weight, q=q, q_out=q_out, cos_sin=cos_sin, rows_out=rows_out)
-    _call("mla_qcache_append_norm_rope", dev, stream, ctypes.byref(desc), _pool(desc, pool),
-          _table(block_table, B, dev), block_table.shape[1], _ints(seq_lens_before, "seq_lens_before", (B,), dev),
-          _ints(new_lens, "new_lens", (B,), dev), pkv, kv_stride, pw, float(eps), pq, q_token, q_head, H, pqo, pcs,
-          cos_sin.shape[0], _ints(positions, "positions", (B, n), dev), _ROPE_PAIRS[convention], prows, B, n)
+        raise ValueError("q_out needs q")
+    if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
+        raise ValueError(f"cos_sin must be a tensor [positions, {D_R}]")
+    positions_held = cos_sin.shape[0]
+    _call("mla_qcache_append_norm_rope", dev, stream, ctypes.byref(desc), _pool(desc, pool, dev),
+          *_table(block_table, B, dev), _arg(seq_lens_before, "seq_lens_before", torch.int32, (B,), dev),
+          _opt(new_lens, "new_lens", torch.int32, (B,), dev), pkv, kv_stride,
+          _opt(norm_weight, "norm_weight", torch.bfloat16, (D_C,), dev), float(eps), pq, q_token, q_head, H, pqo,
+          _arg(cos_sin, "cos_sin", torch.float32, (positions_held, D_R), dev), positions_held,
+          _opt(positions, "positions", torch.int32, (B, n), dev), pairs,
+          _opt(rows_out, "rows_out", torch.bfloat16, (B, n, D_C + D_R), dev), B, n)
     return q_out
 
 
@@ -348,31 +361,30 @@ def mla_qcache_read(desc, pool, block_table, start, cu_rows, max_rows, out_c=Non
     """Read dequantized rows back: tokens start[b] + i (start None: 0) of request b into row
     cu_rows[b] + i of out_c [rows, 512] and out_kr [rows, 64] (bf16; either may be None, and both may
     be column ranges of one buffer). max_rows bounds the rows of one request."""
-    if not isinstance(cu_rows, torch.Tensor) or cu_rows.dim() != 1 or cu_rows.shape[0] < 1:
-        raise ValueError("cu_rows must be a tensor [B + 1]")
-    B, dev = cu_rows.shape[0] - 1, cu_rows.device
-    if out_c is None and out_kr is None:
-        raise ValueError("out_c or out_kr must be given")
-    rows = (out_c if out_c is not None else out_kr).shape[0]
-    pc, sc = (None, 0) if out_c is None else _out_rows(out_c, "out_c", rows, D_C)
-    pr, sr = (None, 0) if out_kr is None else _out_rows(out_kr, "out_kr", rows, D_R)
-    _on(dev, pool=pool, out_c=out_c, out_kr=out_kr)
-    _call("mla_qcache_read", dev, stream, ctypes.byref(desc), _pool(desc, pool), _table(block_table, B, dev),
-          block_table.shape[1], _ints(start, "start", (B,), dev), _ints(cu_rows, "cu_rows", (B + 1,), dev),
+    out = out_c if out_c is not None else out_kr
+    if not isinstance(out, torch.Tensor) or out.dim() != 2:
+        raise ValueError("out_c or out_kr must be given, as tensors [rows, width]")
+    dev = _device_index(cu_rows, "cu_rows", torch.int32, 1)
+    B = cu_rows.shape[0] - 1
+    if B < 0:
+        raise ValueError("cu_rows must have one entry more than there are requests")
+    rows = out.shape[0]
+    pc, sc = (None, 0) if out_c is None else _out_rows(out_c, "out_c", rows, D_C, dev)
+    pr, sr = (None, 0) if out_kr is None else _out_rows(out_kr, "out_kr", rows, D_R, dev)
+    _call("mla_qcache_read", dev, stream, ctypes.byref(desc), _pool(desc, pool, dev), *_table(block_table, B, dev),
+          _opt(start, "start", torch.int32, (B,), dev), _arg(cu_rows, "cu_rows", torch.int32, (B + 1,), dev),
           int(max_rows), rows, pc, sc, pr, sr, B)
 
 
 def mla_page_digest(desc, pool, block_table, seq_lens_before, n_new, digests, *, new_lens=None, stream=None) -> None:
     """Mean keys of the pages that appending new_lens[b] (None: n_new) tokens completed, into the
     pages' rows of digests [num_pages, 576] (bf16). Call it after the append."""
-    if not isinstance(seq_lens_before, torch.Tensor) or seq_lens_before.dim() != 1:
-        raise ValueError("seq_lens_before must be a tensor [B]")
-    B, dev = seq_lens_before.shape[0], seq_lens_before.device
-    pd = _need(digests, "digests", torch.bfloat16, (desc.num_pages, D_C + D_R))
-    _on(dev, pool=pool, digests=digests)
-    _call("mla_page_digest", dev, stream, ctypes.byref(desc), _pool(desc, pool), _table(block_table, B, dev),
-          block_table.shape[1], _ints(seq_lens_before, "seq_lens_before", (B,), dev),
-          _ints(new_lens, "new_lens", (B,), dev), int(n_new), pd, B)
+    dev = _device_index(seq_lens_before, "seq_lens_before", torch.int32, 1)
+    B = seq_lens_before.shape[0]
+    _call("mla_page_digest", dev, stream, ctypes.byref(desc), _pool(desc, pool, dev), *_table(block_table, B, dev),
+          _arg(seq_lens_before, "seq_lens_before", torch.int32, (B,), dev),
+          _opt(new_lens, "new_lens", torch.int32, (B,), dev), int(n_new),
+          _arg(digests, "digests", torch.bfloat16, (desc.num_pages, D_C + D_R), dev), B)
 
 
 def new_digests(desc: mla_qcache_desc, device="cuda") -> torch.Tensor:
@@ -380,33 +392,31 @@ def new_digests(desc: mla_qcache_desc, device="cuda") -> torch.Tensor:
     return torch.zeros((desc.num_pages, D_C + D_R), dtype=torch.bfloat16, device=device)
 
 
-def _page_count(max_seq_len: int) -> int:
-    return -(-int(max_seq_len) // PAGE)
+def _page_count(max_seq_len) -> int:
+    return max(0, -(-max_seq_len // PAGE))
 
 
 def _queries(q_c, q_r):
-    if not isinstance(q_c, torch.Tensor) or q_c.dim() != 4:
-        raise ValueError("q_c must be a tensor [B, s_q, H, 512]")
+    """(B, s_q, H, device index, addresses of q_c and q_r)."""
+    dev = _device_index(q_c, "q_c", torch.bfloat16, 4)
     B, s_q, H = q_c.shape[:3]
-    pc = _need(q_c, "q_c", torch.bfloat16, (B, s_q, H, D_C))
-    return B, s_q, H, pc, _need(q_r, "q_r", torch.bfloat16, (B, s_q, H, D_R))
+    return B, s_q, H, dev, _arg(q_c, "q_c", torch.bfloat16, (B, s_q, H, D_C), dev), \
+        _arg(q_r, "q_r", torch.bfloat16, (B, s_q, H, D_R), dev)
 
 
 def mla_page_scores(block_table, seq_lens, max_seq_len, digests, q_c, q_r, scale, *, out=None, stream=None):
     """Expected attention mass of every candidate page, fp32 [B, s_q, ceil(max_seq_len / 64)] (-inf
     for pages that are no candidates). See include/mla_qcache.h."""
-    B, s_q, H, pc, pr = _queries(q_c, q_r)
-    dev = q_c.device
-    pd = _need(digests, "digests", torch.bfloat16)
-    if digests.dim() != 2 or digests.shape[1] != D_C + D_R:
-        raise ValueError(f"digests must have shape (num_pages, {D_C + D_R}), got {tuple(digests.shape)}")
+    B, s_q, H, dev, pc, pr = _queries(q_c, q_r)
+    max_seq_len = int(max_seq_len)
+    pages = digests.shape[0] if isinstance(digests, torch.Tensor) and digests.dim() == 2 else 0
+    pd = _arg(digests, "digests", torch.bfloat16, (pages, D_C + D_R), dev)
     shape = (B, s_q, _page_count(max_seq_len))
     if out is None:
         out = _empty(shape, torch.float32, dev, stream)
-    po = _need(out, "out", torch.float32, shape)
-    _on(dev, digests=digests, q_r=q_r, out=out)
-    _call("mla_page_scores", dev, stream, pd, digests.shape[0], _table(block_table, B, dev), block_table.shape[1],
-          _ints(seq_lens, "seq_lens", (B,), dev), int(max_seq_len), pc, pr, B, s_q, H, float(scale), po)
+    _call("mla_page_scores", dev, stream, pd, pages, *_table(block_table, B, dev),
+          _arg(seq_lens, "seq_lens", torch.int32, (B,), dev), max_seq_len, pc, pr, B, s_q, H, float(scale),
+          _arg(out, "out", torch.float32, shape, dev))
     return out
 
 
@@ -416,58 +426,57 @@ def mla_select_pages(block_table, seq_lens, max_seq_len, scores, k_pages, *, n_s
     indexes in the request, sel_lens [B, s_q] keys), int32, -1 behind the last page. scores
     [B, s_q, ceil(max_seq_len / 64)] may be None when k_pages covers every page (then s_q is needed).
     sel_table and sel_lens, flattened to B * s_q requests, are what mla_qdecode takes."""
-    if not isinstance(seq_lens, torch.Tensor) or seq_lens.dim() != 1:
-        raise ValueError("seq_lens must be a tensor [B]")
-    B, dev = seq_lens.shape[0], seq_lens.device
-    ps = None
-    if scores is not None:
-        if scores.dim() != 3:
-            raise ValueError("scores must be a tensor [B, s_q, pages]")
+    if scores is None:
+        if s_q is None:
+            raise ValueError("s_q is needed without scores")
+    elif not isinstance(scores, torch.Tensor) or scores.dim() != 3:
+        raise ValueError("scores must be a tensor [B, s_q, pages]")
+    else:
         s_q = scores.shape[1]
-        ps = _need(scores, "scores", torch.float32, (B, s_q, _page_count(max_seq_len)))
-    elif s_q is None:
-        raise ValueError("s_q is needed without scores")
-    k = int(k_pages)
+    dev = _device_index(seq_lens, "seq_lens", torch.int32, 1)
+    B, max_seq_len, k_pages = seq_lens.shape[0], int(max_seq_len), int(k_pages)
+    if k_pages < 1 or s_q < 1:
+        raise MlaError("mla_select_pages", _lib.MLA_ERR_INVALID_ARG)
+    shape = (B, s_q, k_pages)
     if sel_table is None:
-        sel_table = _empty((B, s_q, max(k, 0)), torch.int32, dev, stream)
+        sel_table = _empty(shape, torch.int32, dev, stream)
     if sel_pages is None:
-        sel_pages = _empty((B, s_q, max(k, 0)), torch.int32, dev, stream)
+        sel_pages = _empty(shape, torch.int32, dev, stream)
     if sel_lens is None:
         sel_lens = _empty((B, s_q), torch.int32, dev, stream)
-    _on(dev, scores=scores)
-    _call("mla_select_pages", dev, stream, _table(block_table, B, dev), block_table.shape[1],
-          _ints(seq_lens, "seq_lens", (B,), dev), int(max_seq_len), ps, B, s_q, k, int(n_sink), int(n_recent),
-          _ints(sel_table, "sel_table", (B, s_q, k), dev), _ints(sel_pages, "sel_pages", (B, s_q, k), dev),
-          _ints(sel_lens, "sel_lens", (B, s_q), dev))
+    _call("mla_select_pages", dev, stream, *_table(block_table, B, dev),
+          _arg(seq_lens, "seq_lens", torch.int32, (B,), dev), max_seq_len,
+          _opt(scores, "scores", torch.float32, (B, s_q, _page_count(max_seq_len)), dev), B, s_q, k_pages, int(n_sink), int(n_recent),
+          _arg(sel_table, "sel_table", torch.int32, shape, dev), _arg(sel_pages, "sel_pages", torch.int32, shape, dev),
+          _arg(sel_lens, "sel_lens", torch.int32, (B, s_q), dev))
     return sel_table, sel_pages, sel_lens
 
 
 def mla_qdecode_sparse_workspace_bytes(B, s_q, H, max_seq_len, k_pages) -> int:
-    return int(_lib.load().mla_qdecode_sparse_workspace_bytes(B, s_q, H, int(max_seq_len), int(k_pages)))
+    return _lib.load().mla_qdecode_sparse_workspace_bytes(B, s_q, H, int(max_seq_len), int(k_pages))
 
 
 def mla_qdecode_sparse(desc, pool, block_table, seq_lens, max_seq_len, digests, q_c, q_r, scale, k_pages, *, n_sink=1,
                        n_recent=1, out=None, out_dtype=torch.bfloat16, lse=None, workspace=None, flags=0, stream=None):
     """One decode step over the pages that the digests' scores select (scores, selection, decode).
     digests may be None when k_pages covers every page. Returns (out, lse). See include/mla_qcache.h."""
-    B, s_q, H, pc, pr = _queries(q_c, q_r)
-    dev = q_c.device
-    pd = None if digests is None else _need(digests, "digests", torch.bfloat16, (desc.num_pages, D_C + D_R))
+    B, s_q, H, dev, pc, pr = _queries(q_c, q_r)
+    max_seq_len, k_pages = int(max_seq_len), int(k_pages)
     if out is None:
         out = _empty((B, s_q, H, D_C), out_dtype, dev, stream)
-    if out.dtype not in (torch.bfloat16, torch.float32):
+    f32 = out.dtype is torch.float32
+    if not f32 and out.dtype is not torch.bfloat16:
         raise TypeError("out must be bfloat16 or float32")
-    po = _need(out, "out", out.dtype, (B, s_q, H, D_C))
-    pl = None if lse is None else _need(lse, "lse", torch.float32, (B, s_q, H))
     if workspace is None:
-        workspace = _empty(max(mla_qdecode_sparse_workspace_bytes(B, s_q, H, max_seq_len, k_pages), 1), torch.uint8,
-                           dev, stream)
-    pw = _need(workspace, "workspace", torch.uint8)
-    _on(dev, pool=pool, digests=digests, q_r=q_r, out=out, lse=lse, workspace=workspace)
-    _call("mla_qdecode_sparse", dev, stream, ctypes.byref(desc), _pool(desc, pool), _table(block_table, B, dev),
-          block_table.shape[1], _ints(seq_lens, "seq_lens", (B,), dev), int(max_seq_len), pd, pc, pr, B, s_q, H,
-          float(scale), int(k_pages), int(n_sink), int(n_recent), pw, workspace.numel(), po,
-          int(out.dtype == torch.float32), pl, int(flags))
+        need = mla_qdecode_sparse_workspace_bytes(B, s_q, H, max_seq_len, k_pages)
+        workspace = _empty((max(need, 1),), torch.uint8, dev, stream)
+    nw = workspace.numel()
+    _call("mla_qdecode_sparse", dev, stream, ctypes.byref(desc), _pool(desc, pool, dev), *_table(block_table, B, dev),
+          _arg(seq_lens, "seq_lens", torch.int32, (B,), dev), max_seq_len,
+          _opt(digests, "digests", torch.bfloat16, (desc.num_pages, D_C + D_R), dev), pc, pr, B, s_q, H, float(scale),
+          k_pages, int(n_sink), int(n_recent), _arg(workspace, "workspace", torch.uint8, (nw,), dev), nw,
+          _arg(out, "out", out.dtype, (B, s_q, H, D_C), dev), f32, _opt(lse, "lse", torch.float32, (B, s_q, H), dev),
+          int(flags))
     return out, lse
 
 

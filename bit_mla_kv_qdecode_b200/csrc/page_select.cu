@@ -2,19 +2,21 @@
 // n_recent ones (its own among them) and, up to k pages, those with the highest
 // score, the lower index first among equals; in position order.
 //
-// Every page gets a 32-bit key in the order of its score (pages that are always
-// taken rank above every score, NaN below); the k-th largest key is found two
-// bits at a time by counting, and one ordered pass writes the pages above it
-// and as many equal to it, from the front, as are still wanted.
+// One CTA a query. Every candidate gets a 32-bit key in the order of its score
+// (NaN lowest). The key of the last page taken is found two bits at a time, from
+// the highest bit in which the candidates differ, by counting the keys at or
+// above each of three thresholds: no atomics, one barrier a step, and the search
+// ends when a threshold has exactly the wanted count at or above it. A thread
+// holds consecutive pages in registers, so one scan over the threads gives each
+// page its place. Latency is all there is to it (0.4 MB for 256 queries of up to
+// 512 pages); counting by shared-memory histograms would meet its worst case, equal
+// digits, in every step but the last.
 #include "mla_common.cuh"
 #include "mla_internal.h"
 #include "sm100_ptx.cuh"
 
 namespace mla {
 namespace {
-
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 
 struct SelectArgs {
   const int32_t* table;
@@ -34,12 +36,19 @@ __device__ __forceinline__ uint32_t score_key(float v) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// kItems consecutive pages a thread; a query of more than kItems * kThreads
+// pages is walked in rounds of that many, its keys read again each time.
+template <int kThreads, int kItems>
 __global__ void __launch_bounds__(kThreads) page_select_kernel(const SelectArgs a) {
+  constexpr int kWarps = kThreads / 32, kRound = kThreads * kItems;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  __shared__ int cnt[2][kWarps][4];
-  __shared__ int base[kWarps][2];
+  __shared__ int4 sums[2][kWarps];  // alternating: one barrier between a use's writes and reads, one before its next
+  __shared__ uint2 range[kWarps];
   const int b = blockIdx.y, i = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const size_t q = static_cast<size_t>(b) * a.s_q + i;
+  const float* sc = a.scores + q * a.width;
+  const int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
   int T = __ldg(a.seq_lens + b);
   if (T < 0 || T > a.max_seq_len) {
     if (tid == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
@@ -48,78 +57,149 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(const SelectArgs 
   const int L = T - a.s_q + 1 + i;
   const int n = L > 0 ? (L - 1) / kPage + 1 : 0;  // pages the query sees
   const int take = min(n, a.k);
-  const size_t q = static_cast<size_t>(b) * a.s_q + i;
-  const float* sc = a.scores + q * a.width;
-  auto key = [&](int p) -> uint32_t {
-    if (n <= a.k || p < a.n_sink || p >= n - a.n_recent) return 0xffffffffu;
-    return score_key(__ldg(sc + p));
-  };
-  // the take-th largest key
-  uint32_t thr = 0xffffffffu;
-  int above = 0;  // keys above thr
-  if (n > a.k) {
-    thr = 0u;
-    int round = 0;
-    for (int bit = 30; bit >= 0; bit -= 2, ++round) {
-      int c[4] = {0, 0, 0, 0};
-      for (int p = tid; p < n; p += kThreads) {
-        const uint32_t u = key(p);
+  const bool all = n <= a.k;
+  const int lo = all ? n : a.n_sink, hi = all ? n : n - a.n_recent;  // candidates; the others are taken
+  const int rounds = (n + kRound - 1) / kRound;
+  uint32_t u[kItems];
+  int held = -1;  // round whose keys u holds
+  auto load = [&](int r) {
+    if (held == r) return;
+    held = r;
 #pragma unroll
-        for (int d = 1; d < 4; ++d) c[d] += u >= (thr | (static_cast<uint32_t>(d) << bit));
-      }
-#pragma unroll
-      for (int d = 1; d < 4; ++d) {
-        c[d] = __reduce_add_sync(0xffffffffu, c[d]);
-        if (lane == 0) cnt[round & 1][warp][d] = c[d];
-      }
-      __syncthreads();
-      int t[4] = {0, 0, 0, 0};
-      for (int w = 0; w < kWarps; ++w)
-#pragma unroll
-        for (int d = 1; d < 4; ++d) t[d] += cnt[round & 1][w][d];
-      const uint32_t d = t[3] >= take ? 3u : t[2] >= take ? 2u : t[1] >= take ? 1u : 0u;
-      thr |= d << bit;
+    for (int j = 0; j < kItems; ++j) {
+      const int p = r * kRound + tid * kItems + j;
+      u[j] = p >= lo && p < hi ? score_key(__ldg(sc + p)) : 0u;
     }
-    int c = 0;
-    for (int p = tid; p < n; p += kThreads) c += key(p) > thr;
-    c = __reduce_add_sync(0xffffffffu, c);
+  };
+  // Add up x, y and z over the CTA's warps (one lane each brings them).
+  int step = 0;
+  auto sum3 = [&](int x, int y, int z) {
+    int4* buf = sums[step++ & 1];
+    if (lane == 0) buf[warp] = make_int4(x, y, z, 0);
     __syncthreads();
-    if (lane == 0) cnt[0][warp][0] = c;
+    int3 t = make_int3(0, 0, 0);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const int4 v = buf[w];
+      t.x += v.x;
+      t.y += v.y;
+      t.z += v.z;
+    }
+    return t;
+  };
+  // Keys at or above each of three thresholds, none of them zero.
+  auto count3 = [&](uint32_t t1, uint32_t t2, uint32_t t3) {
+    int s1 = 0, s2 = 0, s3 = 0;
+    for (int r = 0; r < rounds; ++r) {
+      load(r);
+      uint32_t c12 = 0, c3 = 0;  // a warp holds at most 512 keys: two counts a word
+#pragma unroll
+      for (int j = 0; j < kItems; ++j) {
+        c12 += (u[j] >= t1 ? 1u : 0u) + (u[j] >= t2 ? 0x10000u : 0u);
+        c3 += u[j] >= t3 ? 1u : 0u;
+      }
+      c12 = __reduce_add_sync(0xffffffffu, c12);
+      s1 += c12 & 0xffffu;
+      s2 += c12 >> 16;
+      s3 += __reduce_add_sync(0xffffffffu, c3);
+    }
+    return sum3(s1, s2, s3);
+  };
+  const int want = take - (all ? take : a.n_sink + a.n_recent);  // candidates to take
+  uint32_t thr = 0xffffffffu;  // candidates above it are taken, and `ties` equal to it
+  int ties = 0;
+  if (want > 0) {
+    uint32_t mn = 0xffffffffu, mx = 0u;
+    for (int r = 0; r < rounds; ++r) {
+      load(r);
+#pragma unroll
+      for (int j = 0; j < kItems; ++j) {
+        const int p = r * kRound + tid * kItems + j;
+        if (p >= lo && p < hi) {
+          mn = min(mn, u[j]);
+          mx = max(mx, u[j]);
+        }
+      }
+    }
+    mn = __reduce_min_sync(0xffffffffu, mn);
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    if (lane == 0) range[warp] = make_uint2(mn, mx);
     __syncthreads();
-    for (int w = 0; w < kWarps; ++w) above += cnt[0][w][0];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      mn = min(mn, range[w].x);
+      mx = max(mx, range[w].y);
+    }
+    // bits above the highest differing one are common to all candidates
+    int bit = mn == mx ? -2 : (31 - __clz(mn ^ mx)) & ~1;
+    thr = bit < 0 ? mx : bit == 30 ? 0u : mx & ~((4u << bit) - 1u);
+    bool exact = false;  // exactly `want` keys are at or above thr
+    for (; bit >= 0 && !exact; bit -= 2) {
+      const uint32_t t1 = thr | (1u << bit), t2 = thr | (2u << bit), t3 = thr | (3u << bit);
+      const int3 c = count3(t1, t2, t3);
+      const int at = c.z >= want ? c.z : c.y >= want ? c.y : c.x >= want ? c.x : -1;
+      if (at >= 0) thr = c.z >= want ? t3 : c.y >= want ? t2 : t1;
+      exact = at == want;
+    }
+    if (exact) {
+      --thr;  // every key at or above the old one is above this one; it is at least 1 there
+    } else {
+      const int above = thr == 0xffffffffu ? 0 : count3(thr + 1, thr + 1, thr + 1).x;
+      ties = want - above;
+    }
   }
-  const int ties = take - above;  // pages equal to thr that are taken, lowest first
-  // ordered pass: slot = pages above before p + min(ties, equal ones before p)
+  // one ordered pass: a page's place is the number of pages taken before it
   int32_t* out = a.sel_table + q * a.k;
   int32_t* out_pages = a.sel_pages ? a.sel_pages + q * a.k : nullptr;
-  int gt0 = 0, eq0 = 0;
-  for (int p0 = 0; p0 < n; p0 += kThreads) {
-    const int p = p0 + tid;
-    const uint32_t u = p < n ? key(p) : 0u;
-    const bool gt = p < n && u > thr, eq = p < n && u == thr;
-    const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
-    __syncthreads();
-    if (lane == 0) {
-      base[warp][0] = __popc(mg);
-      base[warp][1] = __popc(me);
+  int base = 0, base_eq = 0;  // taken for certain, and equal to thr, in the rounds before
+  for (int r = 0; r < rounds; ++r) {
+    if (want > 0) load(r);
+    int sure = 0, eq = 0;
+    uint32_t is_sure = 0, is_eq = 0;
+#pragma unroll
+    for (int j = 0; j < kItems; ++j) {
+      const int p = r * kRound + tid * kItems + j;
+      const bool cand = p >= lo && p < hi;
+      const bool s = p < n && (!cand || (want > 0 && u[j] > thr));
+      const bool e = cand && want > 0 && ties > 0 && u[j] == thr;
+      is_sure |= static_cast<uint32_t>(s) << j;
+      is_eq |= static_cast<uint32_t>(e) << j;
     }
+    sure = __popc(is_sure);
+    eq = __popc(is_eq);
+    int is = sure, ie = eq;  // inclusive scans over the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, is, o), y = __shfl_up_sync(0xffffffffu, ie, o);
+      if (lane >= o) {
+        is += x;
+        ie += y;
+      }
+    }
+    int4* buf = sums[step++ & 1];
+    if (lane == 31) buf[warp] = make_int4(is, ie, 0, 0);
     __syncthreads();
-    int g = gt0, e = eq0;
+    int s0 = base + is - sure, e0 = base_eq + ie - eq;  // before this thread's pages
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) {
-        g += base[w][0];
-        e += base[w][1];
+        s0 += buf[w].x;
+        e0 += buf[w].y;
       }
-      gt0 += base[w][0];
-      eq0 += base[w][1];
+      base += buf[w].x;
+      base_eq += buf[w].y;
     }
-    const uint32_t below = (1u << lane) - 1;
-    g += __popc(mg & below);
-    e += __popc(me & below);
-    if (gt || (eq && e < ties)) {
-      const int slot = g + min(e, ties);
-      out[slot] = p < a.max_pages ? __ldg(a.table + static_cast<size_t>(b) * a.max_pages + p) : -1;
-      if (out_pages) out_pages[slot] = p;
+#pragma unroll
+    for (int j = 0; j < kItems; ++j) {
+      const int p = r * kRound + tid * kItems + j;
+      const bool s = (is_sure >> j) & 1, e = (is_eq >> j) & 1;
+      if (s || (e && e0 < ties)) {
+        const int slot = s0 + min(e0, ties);
+        out[slot] = __ldg(row + p);
+        if (out_pages) out_pages[slot] = p;
+      }
+      s0 += s;
+      e0 += e;
     }
   }
   for (int s = take + tid; s < a.k; s += kThreads) {
@@ -134,7 +214,12 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(const SelectArgs 
 cudaError_t launch_page_select(const PageSelectLaunch& L) {
   SelectArgs a{L.table, L.seq_lens, L.scores, L.sel_table, L.sel_pages, L.sel_lens, L.status,
                L.max_pages, L.max_seq_len, L.width, L.s_q, L.k_pages, L.n_sink, L.n_recent};
-  return launch_dependent(page_select_kernel, dim3(L.s_q, L.B), dim3(kThreads), 0, L.stream, a);
+  const dim3 grid(L.s_q, L.B);
+  // keys in registers up to 16,384 pages (a million tokens); longer queries read theirs again in each step
+  if (L.width <= 256) return launch_dependent(page_select_kernel<128, 2>, grid, dim3(128), 0, L.stream, a);
+  if (L.width <= 1024) return launch_dependent(page_select_kernel<256, 4>, grid, dim3(256), 0, L.stream, a);
+  if (L.width <= 4096) return launch_dependent(page_select_kernel<512, 8>, grid, dim3(512), 0, L.stream, a);
+  return launch_dependent(page_select_kernel<1024, 16>, grid, dim3(1024), 0, L.stream, a);
 }
 
 }  // namespace mla
