@@ -77,14 +77,11 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(const SelectArgs 
     int4* buf = sums[step++ & 1];
     if (lane == 0) buf[warp] = make_int4(x, y, z, 0);
     __syncthreads();
-    int3 t = make_int3(0, 0, 0);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const int4 v = buf[w];
-      t.x += v.x;
-      t.y += v.y;
-      t.z += v.z;
-    }
+    int3 t;
+    const int4 v = lane < kWarps ? buf[lane] : make_int4(0, 0, 0, 0);
+    t.x = __reduce_add_sync(0xffffffffu, v.x);
+    t.y = __reduce_add_sync(0xffffffffu, v.y);
+    t.z = __reduce_add_sync(0xffffffffu, v.z);
     return t;
   };
   // Keys at or above each of three thresholds, none of them zero.
@@ -109,33 +106,30 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(const SelectArgs 
   uint32_t thr = 0xffffffffu;  // candidates above it are taken, and `ties` equal to it
   int ties = 0;
   if (want > 0) {
-    uint32_t mn = 0xffffffffu, mx = 0u;
+    uint32_t any = 0u, every = 0xffffffffu;
     for (int r = 0; r < rounds; ++r) {
       load(r);
 #pragma unroll
       for (int j = 0; j < kItems; ++j) {
         const int p = r * kRound + tid * kItems + j;
-        if (p >= lo && p < hi) {
-          mn = min(mn, u[j]);
-          mx = max(mx, u[j]);
-        }
+        any |= u[j];
+        every &= p >= lo && p < hi ? u[j] : 0xffffffffu;
       }
     }
-    mn = __reduce_min_sync(0xffffffffu, mn);
-    mx = __reduce_max_sync(0xffffffffu, mx);
-    if (lane == 0) range[warp] = make_uint2(mn, mx);
+    any = __reduce_or_sync(0xffffffffu, any);
+    every = __reduce_and_sync(0xffffffffu, every);
+    if (lane == 0) range[warp] = make_uint2(any, every);
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      mn = min(mn, range[w].x);
-      mx = max(mx, range[w].y);
-    }
-    // bits above the highest differing one are common to all candidates
-    int bit = mn == mx ? -2 : (31 - __clz(mn ^ mx)) & ~1;
-    thr = bit < 0 ? mx : bit == 30 ? 0u : mx & ~((4u << bit) - 1u);
+    any = __reduce_or_sync(0xffffffffu, lane < kWarps ? range[lane].x : 0u);
+    every = __reduce_and_sync(0xffffffffu, lane < kWarps ? range[lane].y : 0xffffffffu);
+    const uint32_t vary = any ^ every;  // bits in which candidates differ; the others need no search
+    thr = every;
+    int bit = 30;
     bool exact = false;  // exactly `want` keys are at or above thr
     for (; bit >= 0 && !exact; bit -= 2) {
-      const uint32_t t1 = thr | (1u << bit), t2 = thr | (2u << bit), t3 = thr | (3u << bit);
+      if ((vary >> bit & 3u) == 0u) continue;
+      const uint32_t base2 = thr & ~(3u << bit);
+      const uint32_t t1 = base2 | (1u << bit), t2 = base2 | (2u << bit), t3 = base2 | (3u << bit);
       const int3 c = count3(t1, t2, t3);
       const int at = c.z >= want ? c.z : c.y >= want ? c.y : c.x >= want ? c.x : -1;
       if (at >= 0) thr = c.z >= want ? t3 : c.y >= want ? t2 : t1;

@@ -4,7 +4,10 @@
 //   rows:    x_hat = bf16(u * s + z)
 //   digest:  kbar_p = bf16( (1/64) sum_t (u_t s_t + z_t) ), fp32 sums
 //
-// u * s is exact in fp32 (at most 15 significant bits), so u * s + z is one rounding.
+// u * s is exact in fp32 (at most 15 significant bits), so u * s + z is one
+// rounding. Codes become floats by setting them into the low bits of 2^23 and
+// subtracting it (both at full rate; the conversion instruction runs at a
+// quarter of it), two values an instruction.
 #include "mla_common.cuh"
 #include "mla_internal.h"
 #include "sm100_ptx.cuh"
@@ -12,10 +15,42 @@
 namespace mla {
 namespace {
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
+// Two fp32 values in one 64-bit register pair.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 make2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
 }
+__device__ __forceinline__ float2 split2(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// Codes k and k + 1 of a packed word as floats.
+template <int BITS>
+__device__ __forceinline__ f32x2 codes2(uint32_t w, int k) {
+  constexpr uint32_t kMask = (1u << BITS) - 1, kBias = 0x4B000000u;  // 2^23
+  const float lo = __uint_as_float((w >> (k * BITS) & kMask) | kBias);
+  const float hi = __uint_as_float((w >> ((k + 1) * BITS) & kMask) | kBias);
+  return add2(make2(lo, hi), make2(-8388608.0f, -8388608.0f));
+}
+__device__ __forceinline__ uint32_t bf16x2(f32x2 v) {
+  const float2 f = split2(v);
+  const __nv_bfloat162 r = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ f32x2 both(float v) { return make2(v, v); }
 
 struct ReadArgs {
   const uint8_t* pool;
@@ -29,63 +64,87 @@ struct ReadArgs {
   int num_pages, max_pages, max_rows;
 };
 
+constexpr int kReadThreads = 256;
+constexpr int kReadTokens = kPage / (kReadThreads / 32);  // tokens of a page a warp takes
+constexpr int kReadBatch = 4;                             // of them in flight at once
+
+// One CTA: the rows of one request that lie in one of its pages, a warp eight
+// tokens. Lane l takes content channels [8l, 8l + 8) and [256 + 8l, 264 + 8l), so
+// that code loads and row stores are contiguous over the warp, and RoPE channels
+// 2l and 2l + 1. Bound: bytes (228-388 read, 1,152 written a token).
 template <int BC, int GC, int BR, int GR>
-__global__ void __launch_bounds__(256) qcache_read_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(kReadThreads) qcache_read_kernel(const ReadArgs a) {
   using G = QGeom<BC, GC, BR, GR>;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, b = blockIdx.y;
-  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y;
   const int r0 = __ldg(a.cu_rows + b), r1 = __ldg(a.cu_rows + b + 1);
-  const int64_t count = static_cast<int64_t>(r1) - r0;
-  if (i == 0 && lane == 0 && (count < 0 || count > a.max_rows || r0 < 0 || r1 > a.total_rows))
-    record_error(a.status, MLA_ERR_INVALID_ARG);
-  if (i >= count || i >= a.max_rows) return;
-  const int64_t row = static_cast<int64_t>(r0) + i;
-  if (row < 0 || row >= a.total_rows) return;
-  const int64_t t = (a.start ? __ldg(a.start + b) : 0) + static_cast<int64_t>(i);
-  const int page = t >= 0 && t <= 0x7fffffff ? lookup_page(a.table, a.max_pages, a.num_pages, b, static_cast<int>(t)) : -1;
-  if (page < 0) {
-    if (lane == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
+  const int64_t first = a.start ? __ldg(a.start + b) : 0;
+  int64_t count = static_cast<int64_t>(r1) - r0;
+  const bool good = r0 >= 0 && count >= 0 && count <= a.max_rows && r1 <= a.total_rows;
+  if (!good || (count > 0 && first < 0)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
+    if (r0 < 0 || first < 0) return;
+    count = min(min(count, static_cast<int64_t>(a.max_rows)), a.total_rows - r0);
+  }
+  const int64_t idx = first / kPage + blockIdx.x;  // page of the request
+  if (idx * kPage >= first + count) return;
+  const int page = idx < a.max_pages ? __ldg(a.table + static_cast<size_t>(b) * a.max_pages + idx) : -1;
+  if (!page_valid(page, a.num_pages)) {
+    if (threadIdx.x == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
     return;
   }
   const uint8_t* pg = a.pool + static_cast<size_t>(page) * G::kPageBytes;
-  const int slot = static_cast<int>(t) % kPage;
-  if (a.out_c) {
-    uint32_t code[2] = {0u, 0u};
-    const uint8_t* crow = pg + G::kOffCC + slot * G::kRowC;
-    if constexpr (BC == 4) {
-      const uint2 v = reinterpret_cast<const uint2*>(crow)[lane];
-      code[0] = v.x;
-      code[1] = v.y;
-    } else {
-      code[0] = reinterpret_cast<const uint32_t*>(crow)[lane];
-    }
-    const uint32_t m = reinterpret_cast<const uint32_t*>(pg + G::kOffCM + slot * G::kGroupsC * 4)[lane * 16 / GC];
-    const float s = half_bits_to_float(m), z = half_bits_to_float(m >> 16);
-    uint32_t o[8];
+  const int64_t row0 = r0 + idx * kPage - first;  // row of the page's first token
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float v[2];
+  for (int t0 = 0; t0 < kReadTokens; t0 += kReadBatch) {
+    uint32_t code[kReadBatch][2], meta[kReadBatch][2], rcode[kReadBatch], rmeta[kReadBatch];
+    bool live[kReadBatch];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int bit = (2 * k + e) * BC;
-        v[e] = fmaf(static_cast<float>((code[bit >> 5] >> (bit & 31)) & ((1u << BC) - 1)), s, z);
+    for (int e = 0; e < kReadBatch; ++e) {
+      const int slot = warp * kReadTokens + t0 + e;
+      const int64_t t = idx * kPage + slot;
+      live[e] = t >= first && t < first + count;
+      if (!live[e]) continue;
+      if (a.out_c) {
+        const uint8_t* crow = pg + G::kOffCC + slot * G::kRowC;
+        const uint32_t* cm = reinterpret_cast<const uint32_t*>(pg + G::kOffCM) + slot * G::kGroupsC;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (BC == 4)
+            code[e][h] = __ldg(reinterpret_cast<const uint32_t*>(crow) + 32 * h + lane);
+          else
+            code[e][h] = __ldg(reinterpret_cast<const uint16_t*>(crow) + 32 * h + lane);
+          meta[e][h] = __ldg(cm + (256 * h + 8 * lane) / GC);
+        }
       }
-      o[k] = pack_bf16(v[0], v[1]);
+      if (a.out_kr) {
+        const uint8_t* rrow = pg + G::kOffRC + slot * G::kRowR;
+        rcode[e] = BR == 4 ? __ldg(rrow + lane) : __ldg(rrow + (lane >> 1)) >> (4 * (lane & 1));
+        rmeta[e] = __ldg(reinterpret_cast<const uint32_t*>(pg + G::kOffRM) + slot * G::kGroupsR + 2 * lane / GR);
+      }
     }
-    uint4* d = reinterpret_cast<uint4*>(a.out_c + row * a.c_stride) + 2 * lane;
-    d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    d[1] = make_uint4(o[4], o[5], o[6], o[7]);
-  }
-  if (a.out_kr) {
-    const uint8_t* rrow = pg + G::kOffRC + slot * G::kRowR;
-    const uint32_t code = BR == 4 ? rrow[lane] : (rrow[lane >> 1] >> (4 * (lane & 1)));
-    const uint32_t m = reinterpret_cast<const uint32_t*>(pg + G::kOffRM + slot * G::kGroupsR * 4)[lane * 2 / GR];
-    const float s = half_bits_to_float(m), z = half_bits_to_float(m >> 16);
-    constexpr uint32_t kMask = (1u << BR) - 1;
-    reinterpret_cast<uint32_t*>(a.out_kr + row * a.kr_stride)[lane] =
-        pack_bf16(fmaf(static_cast<float>(code & kMask), s, z), fmaf(static_cast<float>((code >> BR) & kMask), s, z));
+#pragma unroll
+    for (int e = 0; e < kReadBatch; ++e) {
+      if (!live[e]) continue;
+      const int64_t row = row0 + warp * kReadTokens + t0 + e;
+      if (a.out_c) {
+        uint4* d = reinterpret_cast<uint4*>(a.out_c + row * a.c_stride) + lane;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const f32x2 s = both(half_bits_to_float(meta[e][h])), z = both(half_bits_to_float(meta[e][h] >> 16));
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[k] = bf16x2(fma2(codes2<BC>(code[e][h], 2 * k), s, z));
+          __stcs(d + 32 * h, make_uint4(o[0], o[1], o[2], o[3]));
+        }
+      }
+      if (a.out_kr) {
+        const f32x2 s = both(half_bits_to_float(rmeta[e])), z = both(half_bits_to_float(rmeta[e] >> 16));
+        __stcs(reinterpret_cast<uint32_t*>(a.out_kr + row * a.kr_stride) + lane,
+               bf16x2(fma2(codes2<BR>(rcode[e], 0), s, z)));
+      }
+    }
   }
 }
 
@@ -99,49 +158,100 @@ struct DigestArgs {
   int num_pages, max_pages, n_new;
 };
 
+constexpr int kDigestThreads = 256;
+
+// Sums over tokens of one page part (64 rows of ROW bytes, groups of G channels): a
+// thread takes one 32-bit word's channels over every kSlices-th token; out[c] gets
+// each slice's sum of channel c (slices kStride floats apart).
+template <int BITS, int ROW, int G, int kThreads, int kStride>
+__device__ __forceinline__ void sum_tokens(const uint8_t* codes, const uint8_t* metas, float* out, int tid) {
+  constexpr int kWords = ROW / 4, kCh = 32 / BITS, kGroups = kWords * kCh / G, kSlices = kThreads / kWords;
+  constexpr int kTokens = kPage / kSlices;
+  static_assert(kSlices * kTokens == kPage && kTokens >= 1 && kGroups * G == kWords * kCh, "whole tokens and groups");
+  const int c = tid % kWords, slice = tid / kWords;
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(codes) + c;
+  const uint32_t* m = reinterpret_cast<const uint32_t*>(metas) + c * kCh / G;
+  f32x2 acc[kCh / 2];
+#pragma unroll
+  for (int k = 0; k < kCh / 2; ++k) acc[k] = make2(0.0f, 0.0f);
+  float zsum = 0.0f;
+  constexpr int kBatch = kTokens < 8 ? kTokens : 8;
+#pragma unroll 1
+  for (int t0 = 0; t0 < kTokens; t0 += kBatch) {
+    uint32_t word[kBatch], meta[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int t = (t0 + e) * kSlices + slice;
+      word[e] = __ldg(w + t * kWords);
+      meta[e] = __ldg(m + t * kGroups);
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const f32x2 s = both(half_bits_to_float(meta[e]));
+      zsum += half_bits_to_float(meta[e] >> 16);
+#pragma unroll
+      for (int k = 0; k < kCh / 2; ++k) acc[k] = fma2(codes2<BITS>(word[e], 2 * k), s, acc[k]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kCh / 2; ++k) {
+    const float2 v = split2(add2(acc[k], both(zsum)));
+    *reinterpret_cast<float2*>(out + slice * kStride + c * kCh + 2 * k) = v;
+  }
+}
+
+// One CTA a completed page. Bound: bytes (14,592-24,832 read, 1,152 written a page).
 template <int BC, int GC, int BR, int GR>
-__global__ void __launch_bounds__(kDqk) page_digest_kernel(const DigestArgs a) {
+__global__ void __launch_bounds__(kDigestThreads) page_digest_kernel(const DigestArgs a) {
   using G = QGeom<BC, GC, BR, GR>;
+  constexpr int kSlicesC = kDigestThreads / (G::kRowC / 4), kSlicesR = kDigestThreads / (G::kRowR / 4);
+  __shared__ __align__(16) float part_c[kSlicesC * kDc];
+  __shared__ __align__(16) float part_r[kSlicesR * kDr];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const int b = blockIdx.y, j = threadIdx.x;
+  const int b = blockIdx.y, tid = threadIdx.x;
   const int before = __ldg(a.lens_before + b);
-  int n = a.new_lens ? __ldg(a.new_lens + b) : a.n_new;
+  const int n = a.new_lens ? __ldg(a.new_lens + b) : a.n_new;
   if (before < 0 || n < 0 || n > a.n_new || static_cast<int64_t>(before) + n > 0x7fffffff) {
-    if (blockIdx.x == 0 && j == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
+    if (blockIdx.x == 0 && tid == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
     return;
   }
   const int p = before / kPage + static_cast<int>(blockIdx.x);
   if (p >= (before + n) / kPage) return;
   const int page = lookup_page(a.table, a.max_pages, a.num_pages, b, p * kPage);
   if (page < 0) {
-    if (j == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
+    if (tid == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
     return;
   }
   const uint8_t* pg = a.pool + static_cast<size_t>(page) * G::kPageBytes;
-  const bool content = j < kDc;
-  const int ch = content ? j : j - kDc;
-  const int bits = content ? BC : BR, row = content ? G::kRowC : G::kRowR;
-  const uint8_t* codes = pg + (content ? G::kOffCC : G::kOffRC) + ch * bits / 8;
-  const int shift = ch * bits % 8;
-  const int groups = content ? G::kGroupsC : G::kGroupsR;
-  const uint32_t* meta = reinterpret_cast<const uint32_t*>(pg + (content ? G::kOffCM : G::kOffRM)) + ch / (content ? GC : GR);
-  float sum = 0.0f;
-  for (int t = 0; t < kPage; ++t) {
-    const uint32_t u = (codes[t * row] >> shift) & ((1u << bits) - 1), m = meta[t * groups];
-    sum += fmaf(static_cast<float>(u), half_bits_to_float(m), half_bits_to_float(m >> 16));
+  sum_tokens<BC, G::kRowC, GC, kDigestThreads, kDc>(pg + G::kOffCC, pg + G::kOffCM, part_c, tid);
+  sum_tokens<BR, G::kRowR, GR, kDigestThreads, kDr>(pg + G::kOffRC, pg + G::kOffRM, part_r, tid);
+  __syncthreads();
+  __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.digests + static_cast<size_t>(page) * kDqk);
+  for (int j = tid; j < kDqk / 2; j += kDigestThreads) {
+    const bool content = j < kDc / 2;
+    const float* part = content ? part_c + 2 * j : part_r + 2 * j - kDc;
+    const int slices = content ? kSlicesC : kSlicesR, stride = content ? kDc : kDr;
+    float x = 0.0f, y = 0.0f;
+    for (int s = 0; s < slices; ++s) {
+      const float2 v = *reinterpret_cast<const float2*>(part + s * stride);
+      x += v.x;
+      y += v.y;
+    }
+    dst[j] = __floats2bfloat162_rn(x * (1.0f / kPage), y * (1.0f / kPage));
   }
-  a.digests[static_cast<size_t>(page) * kDqk + j] = __float2bfloat16_rn(sum * (1.0f / kPage));
 }
 
 template <int BC, int GC, int BR, int GR>
 cudaError_t launch_read_t(const ReadLaunch& L, const ReadArgs& a) {
-  return launch_dependent(qcache_read_kernel<BC, GC, BR, GR>, dim3((L.max_rows + 7) / 8, L.B), dim3(256), 0, L.stream, a);
+  return launch_dependent(qcache_read_kernel<BC, GC, BR, GR>, dim3((L.max_rows + 62) / kPage + 1, L.B),
+                          dim3(kReadThreads), 0, L.stream, a);
 }
 
 template <int BC, int GC, int BR, int GR>
 cudaError_t launch_digest_t(const DigestLaunch& L, const DigestArgs& a) {
-  return launch_dependent(page_digest_kernel<BC, GC, BR, GR>, dim3(L.n_new / kPage + 1, L.B), dim3(kDqk), 0, L.stream, a);
+  return launch_dependent(page_digest_kernel<BC, GC, BR, GR>, dim3(L.n_new / kPage + 1, L.B),
+                          dim3(kDigestThreads), 0, L.stream, a);
 }
 
 }  // namespace
