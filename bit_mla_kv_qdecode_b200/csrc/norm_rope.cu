@@ -149,8 +149,9 @@ template <bool kHalf>
 __device__ __forceinline__ void query_warp(const NormRopeArgs& a, int unit, int lane) {
   const int tok = unit / a.head_chunks, chunk = unit - tok * a.head_chunks;
   const int b = tok / a.n_new, j = tok - b * a.n_new;
-  if (a.new_lens && j >= __ldg(a.new_lens + b)) return;
+  const int given = a.new_lens ? __ldg(a.new_lens + b) : a.n_new;
   const int pos = angle_position(a, tok, b, j);
+  if (j >= given) return;
   if (pos < 0) {
     if (lane == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
     return;
@@ -200,7 +201,7 @@ __device__ __forceinline__ void query_warp(const NormRopeArgs& a, int unit, int 
 }
 
 template <int BC, int GC, int BR, int GR, bool kHalf>
-__global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) norm_rope_append_kernel(const NormRopeArgs a) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
