@@ -438,9 +438,11 @@ def mla_select_pages(block_table, seq_lens, max_seq_len, scores, k_pages, *, n_s
     if k_pages < 1 or s_q < 1:
         raise MlaError("mla_select_pages", _lib.MLA_ERR_INVALID_ARG)
     shape = (B, s_q, k_pages)
-    if sel_table is None:
+    if sel_table is None and sel_pages is None:
+        sel_table, sel_pages = _empty((2, *shape), torch.int32, dev, stream).unbind(0)
+    elif sel_table is None:
         sel_table = _empty(shape, torch.int32, dev, stream)
-    if sel_pages is None:
+    elif sel_pages is None:
         sel_pages = _empty(shape, torch.int32, dev, stream)
     if sel_lens is None:
         sel_lens = _empty((B, s_q), torch.int32, dev, stream)

@@ -66,18 +66,23 @@ template <int BC, int GC, int BR, int GR, bool kHalf>
 __device__ __forceinline__ void token_warp(const NormRopeArgs& a, int tok, int lane) {
   using G = QGeom<BC, GC, BR, GR>;
   const int b = tok / a.n_new, j = tok - b * a.n_new;
-  if (a.new_lens && j >= __ldg(a.new_lens + b)) return;
+  // the row and the weights are on their way while the length and the table are looked up
+  const __nv_bfloat16* row = a.kv + static_cast<int64_t>(tok) * a.kv_stride;
+  const uint4* src = reinterpret_cast<const uint4*>(row) + 2 * lane;
+  const uint4 v0 = __ldg(src), v1 = __ldg(src + 1);
+  const uint32_t rw = __ldg(reinterpret_cast<const uint32_t*>(row + kDc) + lane);
+  const uint4* ws = reinterpret_cast<const uint4*>(a.weight) + 2 * lane;
+  const uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+  const uint4 g0 = a.weight ? __ldg(ws) : ones, g1 = a.weight ? __ldg(ws + 1) : ones;
+  const int given = a.new_lens ? __ldg(a.new_lens + b) : a.n_new;
   const int pos = angle_position(a, tok, b, j);
   const int t = __ldg(a.lens_before + b) + j;
+  if (j >= given) return;
   const int page = lookup_page(a.table, a.max_pages, a.num_pages, b, t);
   if (pos < 0 || page < 0) {
     if (lane == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
     return;
   }
-  const __nv_bfloat16* row = a.kv + static_cast<int64_t>(tok) * a.kv_stride;
-  const uint4* src = reinterpret_cast<const uint4*>(row) + 2 * lane;
-  const uint4 v0 = __ldg(src), v1 = __ldg(src + 1);
-  const uint32_t rw = __ldg(reinterpret_cast<const uint32_t*>(row + kDc) + lane);
   const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
   float x[16];
 #pragma unroll
@@ -85,24 +90,18 @@ __device__ __forceinline__ void token_warp(const NormRopeArgs& a, int tok, int l
     x[2 * k] = bf16_lo(w[k]);
     x[2 * k + 1] = bf16_hi(w[k]);
   }
-  double ss = 0.0;
+  double part[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-  for (int k = 0; k < 16; ++k) ss = fma(static_cast<double>(x[k]), static_cast<double>(x[k]), ss);
+  for (int k = 0; k < 16; ++k) part[k & 3] = fma(static_cast<double>(x[k]), static_cast<double>(x[k]), part[k & 3]);
+  double ss = (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const double inv = 1.0 / sqrt(ss / kDc + a.eps);
-  if (a.weight) {
-    const uint4* ws = reinterpret_cast<const uint4*>(a.weight) + 2 * lane;
-    const uint4 g0 = __ldg(ws), g1 = __ldg(ws + 1);
-    const uint32_t g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+  const double inv = rsqrt(ss / kDc + a.eps);
+  const uint32_t g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      x[2 * k] = static_cast<float>(x[2 * k] * inv * static_cast<double>(bf16_lo(g[k])));
-      x[2 * k + 1] = static_cast<float>(x[2 * k + 1] * inv * static_cast<double>(bf16_hi(g[k])));
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 16; ++k) x[k] = static_cast<float>(x[k] * inv);
+  for (int k = 0; k < 8; ++k) {
+    x[2 * k] = static_cast<float>(x[2 * k] * inv * static_cast<double>(bf16_lo(g[k])));
+    x[2 * k + 1] = static_cast<float>(x[2 * k + 1] * inv * static_cast<double>(bf16_hi(g[k])));
   }
 #pragma unroll
   for (int k = 0; k < 16; ++k) x[k] = round_bf16(x[k]);
@@ -165,8 +164,8 @@ __device__ __forceinline__ void query_warp(const NormRopeArgs& a, int unit, int 
   for (int r = 0; r < kHeadsPerWarp / 8; ++r) {
     const int h = chunk * kHeadsPerWarp + 8 * r + (lane >> 2);
     if (h < a.H) {
-      va[r] = *reinterpret_cast<const uint4*>(src + h * a.q_head_stride + ia);
-      vb[r] = *reinterpret_cast<const uint4*>(src + h * a.q_head_stride + ib);
+      va[r] = __ldcs(reinterpret_cast<const uint4*>(src + h * a.q_head_stride + ia));
+      vb[r] = __ldcs(reinterpret_cast<const uint4*>(src + h * a.q_head_stride + ib));
     }
   }
   const float4* cs = reinterpret_cast<const float4*>(a.cos_sin + static_cast<int64_t>(pos) * kDr + 8 * i);

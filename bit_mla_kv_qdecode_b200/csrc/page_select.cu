@@ -3,14 +3,14 @@
 // score, the lower index first among equals; in position order.
 //
 // One CTA a query. Every candidate gets a 32-bit key in the order of its score
-// (NaN lowest). The key of the last page taken is found two bits at a time, from
-// the highest bit in which the candidates differ, by counting the keys at or
-// above each of three thresholds: no atomics, one barrier a step, and the search
-// ends when a threshold has exactly the wanted count at or above it. A thread
-// holds consecutive pages in registers, so one scan over the threads gives each
-// page its place. Latency is all there is to it (0.4 MB for 256 queries of up to
-// 512 pages); counting by shared-memory histograms would meet its worst case, equal
-// digits, in every step but the last.
+// (NaN lowest). The key of the last page taken is found two bits at a time, over
+// the bits in which candidates differ, by counting the keys at or above each of
+// three thresholds: one barrier a step, and the search ends when a threshold has
+// exactly the wanted count at or above it. A thread holds consecutive pages in
+// registers, so one scan over the threads gives each page its place. Latency is
+// all there is to it (0.4 MB for 256 queries of up to 512 pages, 6.5 us);
+// counting in histograms would meet its worst case, equal digits, whenever many
+// scores are equal.
 #include "mla_common.cuh"
 #include "mla_internal.h"
 #include "sm100_ptx.cuh"
@@ -43,8 +43,9 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(const SelectArgs 
   constexpr int kWarps = kThreads / 32, kRound = kThreads * kItems;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  __shared__ int4 sums[2][kWarps];  // alternating: one barrier between a use's writes and reads, one before its next
+  __shared__ uint32_t sums[3][3];
   __shared__ uint2 range[kWarps];
+  __shared__ int2 scan[2][kWarps];
   const int b = blockIdx.y, i = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const size_t q = static_cast<size_t>(b) * a.s_q + i;
   const float* sc = a.scores + q * a.width;
@@ -71,36 +72,36 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(const SelectArgs 
       u[j] = p >= lo && p < hi ? score_key(__ldg(sc + p)) : 0u;
     }
   };
-  // Add up x, y and z over the CTA's warps (one lane each brings them).
+  // Keys at or above each of three thresholds, none of them zero, over the CTA.
+  // Three buffers in turn: one in use, one being read by late warps, one cleared
+  // for the next. Two counts share a word where a query's pages fit 16 bits.
+  constexpr bool kWide = kRound > 8192;  // the instance that takes any number of pages
   int step = 0;
-  auto sum3 = [&](int x, int y, int z) {
-    int4* buf = sums[step++ & 1];
-    if (lane == 0) buf[warp] = make_int4(x, y, z, 0);
-    __syncthreads();
-    int3 t;
-    const int4 v = lane < kWarps ? buf[lane] : make_int4(0, 0, 0, 0);
-    t.x = __reduce_add_sync(0xffffffffu, v.x);
-    t.y = __reduce_add_sync(0xffffffffu, v.y);
-    t.z = __reduce_add_sync(0xffffffffu, v.z);
-    return t;
-  };
-  // Keys at or above each of three thresholds, none of them zero.
   auto count3 = [&](uint32_t t1, uint32_t t2, uint32_t t3) {
-    int s1 = 0, s2 = 0, s3 = 0;
+    uint32_t c1 = 0, c2 = 0, c3 = 0;
     for (int r = 0; r < rounds; ++r) {
       load(r);
-      uint32_t c12 = 0, c3 = 0;  // a warp holds at most 512 keys: two counts a word
 #pragma unroll
       for (int j = 0; j < kItems; ++j) {
-        c12 += (u[j] >= t1 ? 1u : 0u) + (u[j] >= t2 ? 0x10000u : 0u);
+        c1 += (u[j] >= t1 ? 1u : 0u) + (!kWide && u[j] >= t2 ? 0x10000u : 0u);
+        if (kWide) c2 += u[j] >= t2 ? 1u : 0u;
         c3 += u[j] >= t3 ? 1u : 0u;
       }
-      c12 = __reduce_add_sync(0xffffffffu, c12);
-      s1 += c12 & 0xffffu;
-      s2 += c12 >> 16;
-      s3 += __reduce_add_sync(0xffffffffu, c3);
     }
-    return sum3(s1, s2, s3);
+    c1 = __reduce_add_sync(0xffffffffu, c1);
+    if (kWide) c2 = __reduce_add_sync(0xffffffffu, c2);
+    c3 = __reduce_add_sync(0xffffffffu, c3);
+    uint32_t* buf = sums[step % 3];
+    uint32_t* next = sums[(step + 1) % 3];
+    ++step;
+    if (lane == 0) {
+      atomicAdd(buf, c1);
+      if (kWide) atomicAdd(buf + 1, c2);
+      atomicAdd(buf + 2, c3);
+    }
+    if (tid < 3) next[tid] = 0u;
+    __syncthreads();
+    return kWide ? make_int3(buf[0], buf[1], buf[2]) : make_int3(buf[0] & 0xffffu, buf[0] >> 16, buf[2]);
   };
   const int want = take - (all ? take : a.n_sink + a.n_recent);  // candidates to take
   uint32_t thr = 0xffffffffu;  // candidates above it are taken, and `ties` equal to it
@@ -119,6 +120,7 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(const SelectArgs 
     any = __reduce_or_sync(0xffffffffu, any);
     every = __reduce_and_sync(0xffffffffu, every);
     if (lane == 0) range[warp] = make_uint2(any, every);
+    if (tid < 3) sums[0][tid] = 0u;
     __syncthreads();
     any = __reduce_or_sync(0xffffffffu, lane < kWarps ? range[lane].x : 0u);
     every = __reduce_and_sync(0xffffffffu, lane < kWarps ? range[lane].y : 0xffffffffu);
@@ -170,8 +172,8 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(const SelectArgs 
         ie += y;
       }
     }
-    int4* buf = sums[step++ & 1];
-    if (lane == 31) buf[warp] = make_int4(is, ie, 0, 0);
+    int2* buf = scan[r & 1];
+    if (lane == 31) buf[warp] = make_int2(is, ie);
     __syncthreads();
     int s0 = base + is - sure, e0 = base_eq + ie - eq;  // before this thread's pages
 #pragma unroll
@@ -209,10 +211,15 @@ cudaError_t launch_page_select(const PageSelectLaunch& L) {
   SelectArgs a{L.table, L.seq_lens, L.scores, L.sel_table, L.sel_pages, L.sel_lens, L.status,
                L.max_pages, L.max_seq_len, L.width, L.s_q, L.k_pages, L.n_sink, L.n_recent};
   const dim3 grid(L.s_q, L.B);
-  // keys in registers up to 16,384 pages (a million tokens); longer queries read theirs again in each step
+  // Keys in registers up to 16,384 pages (a million tokens); longer queries read
+  // theirs again in each step. Few keys a thread keep a step short, few warps its
+  // barrier (2,048 pages: 6.7 us with 512 threads, 8.7 with eight keys each on 512,
+  // 9.7 with sixteen on 256, 10.2 with four on 1,024).
   if (L.width <= 256) return launch_dependent(page_select_kernel<128, 2>, grid, dim3(128), 0, L.stream, a);
   if (L.width <= 1024) return launch_dependent(page_select_kernel<256, 4>, grid, dim3(256), 0, L.stream, a);
+  if (L.width <= 2048) return launch_dependent(page_select_kernel<512, 4>, grid, dim3(512), 0, L.stream, a);
   if (L.width <= 4096) return launch_dependent(page_select_kernel<512, 8>, grid, dim3(512), 0, L.stream, a);
+  if (L.width <= 8192) return launch_dependent(page_select_kernel<1024, 8>, grid, dim3(1024), 0, L.stream, a);
   return launch_dependent(page_select_kernel<1024, 16>, grid, dim3(1024), 0, L.stream, a);
 }
 

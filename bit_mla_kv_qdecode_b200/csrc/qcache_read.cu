@@ -184,99 +184,234 @@ struct DigestArgs {
   int num_pages, max_pages, n_new;
 };
 
-constexpr int kDigestThreads = 256;
+// The sums on warp-level MMAs: sum_t u_t s_t over a page's 64 tokens is a product
+// of the steps (one row for each group of channels) with the codes (tokens x
+// channels), both exact in fp16, accumulated in fp32. Two tokens' codes become a
+// pair of fp16 values in place, by setting them into the low bits of 1024 and
+// subtracting it, 1.6 instructions a value with all loads (fp32 multiply-adds on
+// the vector unit took 4.5: 19.3 us for the 2,048 pages of a prefill, bound by
+// their issue). Nine warps, each with 64 channels of its own and no exchange.
+constexpr int kDigestWarps = 9;  // eight of the content, one of the RoPE part
+constexpr int kDigestThreads = 32 * kDigestWarps;
 
-// Sums over tokens of one page part (64 rows of ROW bytes of codes, groups of G
-// channels): a thread takes one 32-bit word's channels of every kSlices-th token.
-template <int BITS, int ROW, int G>
-struct TokenSums {
-  static constexpr int kWords = ROW / 4, kCh = 32 / BITS, kGroups = kWords * kCh / G;
-  static constexpr int kSlices = kDigestThreads / kWords, kTokens = kPage / kSlices;
-  static constexpr int kParts = kWords < 32 ? kDigestThreads / 32 : kSlices;  // left after the sum within a warp
-  static_assert(kSlices * kTokens == kPage && kTokens >= 1 && kGroups * G == kWords * kCh, "whole tokens and groups");
-  uint32_t word[kTokens], meta[kTokens];
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
-  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* metas, int tid) {
-    const int c = tid % kWords, slice = tid / kWords;
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(codes) + slice * kWords + c;
-    const uint32_t* m = reinterpret_cast<const uint32_t*>(metas) + slice * kGroups + c * kCh / G;
+// c[16 x 8] += a[16 x 16] b[16 x 8], rows 8-15 of a zero (and so c[2] and c[3]).
+__device__ __forceinline__ void mma_steps(float (&c)[4], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(0u), "r"(a2), "r"(0u), "r"(b0), "r"(b1));
+}
+
+// Mean over a page's tokens of the 64 channels from 64 * part on, of codes of BITS
+// in rows of CHANNELS with groups of G; out: their bf16 values.
+template <int BITS, int CHANNELS, int G, bool kShared>
+__device__ __forceinline__ void mean_of_tokens(const uint8_t* codes, const uint8_t* metas, int part, __nv_bfloat16* out,
+                                               int lane) {
+  constexpr int kRow = CHANNELS * BITS / 8, kGroups = CHANNELS / G, kMine = 64 / G;  // groups of the warp: 1 or 2
+  const int q = lane & 3, r = lane >> 2;
+  auto load_meta = [&](int t, int g) -> uint32_t {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(metas) + t * kGroups + kMine * part + g;
+    return kShared ? *p : __ldg(p);
+  };
+  // eight codes of token t, unit r of the warp's channels
+  auto load_unit = [&](int t) -> uint32_t {
+    if constexpr (BITS == 4) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(codes + t * kRow) + 8 * part + r;
+      return kShared ? *p : __ldg(p);
+    } else {
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(codes + t * kRow) + 8 * part + r;
+      return kShared ? *p : __ldg(p);
+    }
+  };
+  uint32_t w[4][4], m[4][4];  // K-step, token 2q + {0, 1, 8, 9} of it
 #pragma unroll
-    for (int e = 0; e < kTokens; ++e) {
-      word[e] = __ldg(w + e * kSlices * kWords);
-      meta[e] = __ldg(m + e * kSlices * kGroups);
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int t = 16 * k + 2 * q + (e & 1) + 8 * (e >> 1);
+      w[k][e] = load_unit(t);
+      m[k][e] = r < kMine ? load_meta(t, r) : 0u;
+    }
+  float z[kMine];  // offsets, over the tokens
+#pragma unroll
+  for (int g = 0; g < kMine; ++g)
+    z[g] = half_bits_to_float(load_meta(lane, g) >> 16) + half_bits_to_float(load_meta(lane + 32, g) >> 16);
+  float acc[8][4] = {};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t a0 = __byte_perm(m[k][0], m[k][1], 0x5410), a2 = __byte_perm(m[k][2], m[k][3], 0x5410);
+    // 16 bits of each of two tokens: all of INT2's eight codes, or four of INT4's
+#pragma unroll
+    for (int half = 0; half < BITS / 2; ++half) {
+      const uint32_t sel = half ? 0x7632 : 0x5410;
+      const uint32_t p0 = __byte_perm(w[k][0], w[k][1], sel), p1 = __byte_perm(w[k][2], w[k][3], sel);
+      constexpr int kCodes = 16 / BITS, kInPlace = BITS == 4 ? 2 : 5;  // codes within the low ten bits
+#pragma unroll
+      for (int j = 0; j < kCodes; ++j) {
+        const int down = j < kInPlace ? 0 : kInPlace * BITS;
+        const uint32_t mask = ((1u << BITS) - 1) * 0x00010001u << (j * BITS - down);
+        const uint32_t b0 = hadd2((p0 >> down & mask) | 0x64006400u, 0xE400E400u);  // 1024 + ..., less 1024
+        const uint32_t b1 = hadd2((p1 >> down & mask) | 0x64006400u, 0xE400E400u);
+        mma_steps(acc[half * kCodes + j], a0, a2, b0, b1);
+      }
     }
   }
-  // out[part][channel]: the sums of kParts sets of tokens
-  __device__ __forceinline__ void sum(float* out, int tid) {
-    f32x2 acc[kCh / 2];
 #pragma unroll
-    for (int k = 0; k < kCh / 2; ++k) acc[k] = make2(0.0f, 0.0f);
-    float zsum = 0.0f;
+  for (int g = 0; g < kMine; ++g)
 #pragma unroll
-    for (int e = 0; e < kTokens; ++e) {
-      const Steps<BITS> s(half_bits_to_float(meta[e]));
-      zsum += half_bits_to_float(meta[e] >> 16);
+    for (int o = 16; o > 0; o >>= 1) z[g] += __shfl_xor_sync(0xffffffffu, z[g], o);
+  // lane 4g + q holds units 2q and 2q + 1 against the steps of group g
+  if (r >= kMine || 2 * q / (8 / kMine) != r) return;
+  const float zr = r == 0 ? z[0] : z[kMine - 1];
 #pragma unroll
-      for (int k = 0; k < kCh / 2; ++k)  // 16 bits of codes at a time
-        acc[k] = fma2(fields2<BITS>(word[e] >> (16 * (k / (8 / BITS))), 2 * k % (16 / BITS)), s.v[k % (8 / BITS)], acc[k]);
+  for (int e = 0; e < 2; ++e) {
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      float v[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        constexpr int kCodes = 16 / BITS, kInPlace = BITS == 4 ? 2 : 5;
+        const int c = (j + i) % kCodes, place = c < kInPlace ? c : c - kInPlace;  // the value stood 2^(BITS place) too high
+        v[i] = fmaf(acc[j + i][e], 1.0f / (1 << (BITS * place)), zr) * (1.0f / kPage);
+      }
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[0], v[1]);
+      o[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    const int c = tid % kWords, part = kWords < 32 ? tid / 32 : tid / kWords;
-#pragma unroll
-    for (int k = 0; k < kCh / 2; ++k) {
-      acc[k] = add2(acc[k], both(zsum));
-#pragma unroll
-      for (int o = kWords; o < 32; o <<= 1) acc[k] = add2(acc[k], __shfl_xor_sync(0xffffffffu, acc[k], o));
-      if (kWords >= 32 || tid % 32 < kWords)
-        *reinterpret_cast<float2*>(out + part * (kWords * kCh) + c * kCh + 2 * k) = split2(acc[k]);
-    }
+    reinterpret_cast<uint4*>(out + 64 * part)[2 * q + e] = make_uint4(o[0], o[1], o[2], o[3]);
   }
-};
+}
 
-// One CTA a completed page. Bound: bytes (14,592-24,832 read, 1,152 written a page).
-template <int BC, int GC, int BR, int GR>
-__global__ void __launch_bounds__(kDigestThreads) page_digest_kernel(const DigestArgs a) {
-  using G = QGeom<BC, GC, BR, GR>;
-  using SumC = TokenSums<BC, G::kRowC, GC>;
-  using SumR = TokenSums<BR, G::kRowR, GR>;
-  __shared__ __align__(16) float part_c[SumC::kParts * kDc];
-  __shared__ __align__(16) float part_r[SumR::kParts * kDr];
-  ptx::griddep_wait();
-  ptx::griddep_launch_dependents();
-  const int b = blockIdx.y, tid = threadIdx.x;
+// Page of the x-th completed page of request b, or -1; bad lengths and table
+// entries are flagged.
+__device__ __forceinline__ int completed_page(const DigestArgs& a, int b, int x) {
   const int before = __ldg(a.lens_before + b);
   const int n = a.new_lens ? __ldg(a.new_lens + b) : a.n_new;
   if (before < 0 || n < 0 || n > a.n_new || static_cast<int64_t>(before) + n > 0x7fffffff) {
-    if (blockIdx.x == 0 && tid == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
-    return;
+    if (x == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
+    return -1;
   }
-  const int p = before / kPage + static_cast<int>(blockIdx.x);
-  if (p >= (before + n) / kPage) return;
+  const int p = before / kPage + x;
+  if (p >= (before + n) / kPage) return -1;
   const int page = lookup_page(a.table, a.max_pages, a.num_pages, b, p * kPage);
-  if (page < 0) {
-    if (tid == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
+  if (page < 0) record_error(a.status, MLA_ERR_INVALID_ARG);
+  return page;
+}
+
+// One warp's share of a page's digest.
+template <int BC, int GC, int BR, int GR, bool kShared>
+__device__ __forceinline__ void digest_warp(const uint8_t* pg, __nv_bfloat16* row, int warp, int lane) {
+  using G = QGeom<BC, GC, BR, GR>;
+  if (warp < 8)
+    mean_of_tokens<BC, kDc, GC, kShared>(pg + G::kOffCC, pg + G::kOffCM, warp, row, lane);
+  else
+    mean_of_tokens<BR, kDr, GR, kShared>(pg + G::kOffRC, pg + G::kOffRM, 0, row + kDc, lane);
+}
+
+// Few pages (a decode step): one CTA for each that may be complete.
+template <int BC, int GC, int BR, int GR>
+__global__ void __launch_bounds__(kDigestThreads) page_digest_kernel(const DigestArgs a) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const int page = completed_page(a, blockIdx.y, blockIdx.x);
+  if (page < 0) return;
+  digest_warp<BC, GC, BR, GR, false>(a.pool + static_cast<size_t>(page) * QGeom<BC, GC, BR, GR>::kPageBytes,
+                                     a.digests + static_cast<size_t>(page) * kDqk, threadIdx.x >> 5, threadIdx.x & 31);
+}
+
+// Many pages (after a prefill): two CTAs an SM walk the pages, one warp looking up
+// 32 of them at a time and copying each whole page (it is contiguous) into a
+// ring, nine warps summing from there. A CTA a page spends most of its time in
+// three dependent round trips to memory. Bound: bytes (14,592-24,832 read, 1,152
+// written a page).
+constexpr int kRingPages = 4, kRingCtas = 2;
+constexpr uint64_t kRingWaitNs = 2000000000ull;
+
+template <int kPageBytes>
+struct DigestRing {
+  alignas(128) uint8_t pages[kRingPages][(kPageBytes + 127) / 128 * 128];
+  uint64_t full[kRingPages], empty[kRingPages];
+  int page[kRingPages];
+  int abort;
+};
+
+template <int BC, int GC, int BR, int GR>
+__global__ void __launch_bounds__(kDigestThreads + 32, kRingCtas) page_digest_ring_kernel(const DigestArgs a, int per_request,
+                                                                                 int items) {
+  constexpr int kPageBytes = QGeom<BC, GC, BR, GR>::kPageBytes;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  DigestRing<kPageBytes>& m = *reinterpret_cast<DigestRing<kPageBytes>*>(smem_raw);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kRingPages; ++s) {
+      ptx::mbar_init(&m.full[s], 1);
+      ptx::mbar_init(&m.empty[s], kDigestWarps);
+    }
+    m.abort = 0;
+    ptx::fence_mbar_init_cluster();
+  }
+  __syncthreads();
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  volatile int* abort_flag = &m.abort;
+  // A whole warp waits; one whose wait runs out flags it, and all warps leave.
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort_flag, kRingWaitNs));
+    if (!ok) {
+      *abort_flag = 1;
+      if (lane == 0) record_error(a.status, MLA_ERR_TIMEOUT);
+    }
+    return ok;
+  };
+  if (warp == kDigestWarps) {  // the copying warp
+    int it = 0;
+    bool ok = true;
+    auto next_slot = [&] {  // free once the summing warps have left it
+      const int s = it % kRingPages, round = it / kRingPages;
+      ++it;
+      ok = round == 0 || wait(&m.empty[s], (round - 1) & 1);
+      return s;
+    };
+    for (int64_t i0 = blockIdx.x; ok && i0 < items; i0 += 32ll * gridDim.x) {
+      const int64_t i = i0 + static_cast<int64_t>(lane) * gridDim.x;
+      const int mine = i < items ? completed_page(a, static_cast<int>(i / per_request), static_cast<int>(i % per_request)) : -1;
+      for (uint32_t left = __ballot_sync(0xffffffffu, mine >= 0); ok && left; left &= left - 1) {
+        const int page = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
+        const int s = next_slot();
+        if (ok && lane == 0) {
+          m.page[s] = page;
+          ptx::mbar_arrive_expect_tx(&m.full[s], kPageBytes);
+          ptx::bulk_load(m.pages[s], a.pool + static_cast<size_t>(page) * kPageBytes, kPageBytes, &m.full[s]);
+        }
+      }
+    }
+    if (ok) {
+      const int s = next_slot();
+      if (ok && lane == 0) {
+        m.page[s] = -1;  // the end
+        ptx::mbar_arrive(&m.full[s]);
+      }
+    }
+    if (!ok) {  // copies in flight get time to land before the memory is given back
+      const uint64_t t0 = ptx::globaltimer_ns();
+      while (ptx::globaltimer_ns() - t0 < 100000ull) {
+      }
+    }
     return;
   }
-  const uint8_t* pg = a.pool + static_cast<size_t>(page) * G::kPageBytes;
-  SumC content;
-  SumR rope;
-  content.load(pg + G::kOffCC, pg + G::kOffCM, tid);
-  rope.load(pg + G::kOffRC, pg + G::kOffRM, tid);
-  content.sum(part_c, tid);
-  rope.sum(part_r, tid);
-  __syncthreads();
-  __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.digests + static_cast<size_t>(page) * kDqk);
-  for (int j = tid; j < kDqk / 2; j += kDigestThreads) {
-    const bool in_c = j < kDc / 2;
-    const float* part = in_c ? part_c + 2 * j : part_r + 2 * j - kDc;
-    const int parts = in_c ? SumC::kParts : SumR::kParts, stride = in_c ? kDc : kDr;
-    float x = 0.0f, y = 0.0f;
-#pragma unroll 4
-    for (int s = 0; s < parts; ++s) {
-      const float2 v = *reinterpret_cast<const float2*>(part + s * stride);
-      x += v.x;
-      y += v.y;
-    }
-    dst[j] = __floats2bfloat162_rn(x * (1.0f / kPage), y * (1.0f / kPage));
+  for (int it = 0;; ++it) {
+    const int s = it % kRingPages;
+    if (!wait(&m.full[s], (it / kRingPages) & 1)) break;
+    const int page = m.page[s];
+    if (page < 0) break;
+    digest_warp<BC, GC, BR, GR, true>(m.pages[s], a.digests + static_cast<size_t>(page) * kDqk, warp, lane);
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&m.empty[s]);
   }
 }
 
@@ -293,8 +428,20 @@ cudaError_t launch_read_t(const ReadLaunch& L, const ReadArgs& a) {
 
 template <int BC, int GC, int BR, int GR>
 cudaError_t launch_digest_t(const DigestLaunch& L, const DigestArgs& a) {
-  return launch_dependent(page_digest_kernel<BC, GC, BR, GR>, dim3(L.n_new / kPage + 1, L.B),
-                          dim3(kDigestThreads), 0, L.stream, a);
+  const int per_request = L.n_new / kPage + 1;
+  const int64_t items = static_cast<int64_t>(per_request) * L.B;
+  if (items < 4 * 148 || items > 0x7fffffff)
+    return launch_dependent(page_digest_kernel<BC, GC, BR, GR>, dim3(per_request, L.B), dim3(kDigestThreads), 0, L.stream, a);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  auto kern = page_digest_ring_kernel<BC, GC, BR, GR>;
+  constexpr int kSmem = sizeof(DigestRing<QGeom<BC, GC, BR, GR>::kPageBytes>);
+  static_assert(kRingCtas * (kSmem + 1024) <= 233472, "CTAs an SM");
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3(kRingCtas * sms), dim3(kDigestThreads + 32), kSmem, L.stream, a, per_request,
+                          static_cast<int>(items));
 }
 
 }  // namespace

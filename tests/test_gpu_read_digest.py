@@ -133,6 +133,37 @@ def _digest_case(fmt, before, n, new_lens=None, seed=0):
         assert np.all(np.abs(got[p] - want) <= tol)
 
 
+@pytest.mark.parametrize("fmt", [(4, 64, 4, 64), (2, 32, 4, 64), (2, 64, 2, 32)])
+def test_digest_many_pages(fmt):
+    """More pages than one CTA each would do at once: ragged prompts, some of them empty."""
+    rng = np.random.default_rng(6)
+    n, B = 64 * 40, 24
+    given = rng.integers(0, n + 1, B)
+    given[:4] = n, 0, 63, 64
+    _digest_case(fmt, rng.integers(0, 200, B), n, list(given), seed=3)
+
+
+def test_digest_many_pages_with_bad_ones():
+    rng = np.random.default_rng(7)
+    fmt, B, n = (4, 64, 4, 64), 40, 64 * 20
+    pages = 30
+    pool = torch.from_numpy(ref.random_pool(rng, fmt, pages)).cuda()
+    desc = api.make_desc(*fmt, num_pages=pages)
+    table = np.full((B, 20), pages + 1)
+    table[3, :20] = np.arange(20)
+    table[7, 5] = 25
+    before = np.zeros(B)
+    before[9] = -1
+    out = torch.full((pages, 576), 7.0, dtype=torch.bfloat16).cuda()
+    api.mla_page_digest(desc, pool, _i32(table), _i32(before), n, out)
+    assert api.mla_get_device_status() == api._lib.MLA_ERR_INVALID_ARG
+    alone = torch.full_like(out, 7.0)
+    api.mla_page_digest(desc, pool, _i32(np.arange(20)[None]), _i32([0]), n, alone)
+    api.mla_page_digest(desc, pool, _i32([[25]]), _i32([0]), 64, alone)
+    assert api.mla_get_device_status() == 0
+    assert torch.equal(out, alone)
+
+
 def test_digest_bad_data_is_skipped():
     rng = np.random.default_rng(4)
     fmt = (4, 64, 4, 64)

@@ -128,7 +128,7 @@ def _select_case(scores, lens, k, n_sink, n_recent, seed=0):
 @pytest.mark.parametrize("lens,s_q,k,n_sink,n_recent", [
     ([1], 1, 1, 0, 1), ([5000, 64, 65, 3], 1, 8, 1, 2), ([5000, 200], 3, 16, 0, 1), ([70000], 1, 300, 4, 8),
     ([64 * 1025, 64 * 1024, 64 * 256 + 1], 2, 64, 2, 2), ([4096] * 3, 1, 64, 1, 1), ([4096] * 3, 1, 63, 31, 32),
-    ([64 * 20000 + 9], 1, 777, 1, 1), ([1, 2, 3], 4, 5, 0, 1), ([64 * 300], 1, 1, 0, 1), ([64 * 5000] * 2, 1, 4096, 3, 3)])
+    ([64 * 20000 + 9], 1, 777, 1, 1), ([64 * 70000], 1, 66000, 1, 1), ([64 * 7000], 1, 500, 1, 1), ([1, 2, 3], 4, 5, 0, 1), ([64 * 300], 1, 1, 0, 1), ([64 * 5000] * 2, 1, 4096, 3, 3)])
 def test_select(lens, s_q, k, n_sink, n_recent):
     rng = np.random.default_rng(len(lens) + k)
     W = -(-max(lens) // 64)
