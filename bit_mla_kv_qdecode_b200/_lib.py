@@ -81,10 +81,10 @@ SIGNATURES = {
                                  _c_int, _c_float, _c_void, _c_void]),
     "mla_select_pages": (_c_int, [_c_void, _c_int, _c_void, _c_int, _c_void, _c_int, _c_int, _c_int, _c_int, _c_int,
                                   _c_void, _c_void, _c_void, _c_void]),
-    "mla_qdecode_sparse_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int]),
+    "mla_qdecode_sparse_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int]),
     "mla_qdecode_sparse": (_c_int, [_P, _c_void, _c_void, _c_int, _c_void, _c_int, _c_void, _c_void, _c_void, _c_int,
-                                    _c_int, _c_int, _c_float, _c_int, _c_int, _c_int, _c_void, _c_size, _c_void, _c_int,
-                                    _c_void, _c_uint, _c_void]),
+                                    _c_int, _c_int, _c_float, _c_int, _c_int, _c_int, _c_int, _c_void, _c_size, _c_void,
+                                    _c_int, _c_void, _c_uint, _c_void]),
     "mla_cache_bytes_per_request": (_c_size, [_P, ctypes.c_long, _c_int, _c_int]),
     "mla_cache_max_requests": (ctypes.c_long, [_P, ctypes.c_long, _c_int, _c_int, _c_size]),
     "mla_get_device_status": (_c_int, [ctypes.POINTER(_c_int), _c_void]),

@@ -454,12 +454,13 @@ def mla_select_pages(block_table, seq_lens, max_seq_len, scores, k_pages, *, n_s
     return sel_table, sel_pages, sel_lens
 
 
-def mla_qdecode_sparse_workspace_bytes(B, s_q, H, max_seq_len, k_pages) -> int:
-    return _lib.load().mla_qdecode_sparse_workspace_bytes(B, s_q, H, int(max_seq_len), int(k_pages))
+def mla_qdecode_sparse_workspace_bytes(B, s_q, H, max_seq_len, k_pages, num_splits=0) -> int:
+    return _lib.load().mla_qdecode_sparse_workspace_bytes(B, s_q, H, int(max_seq_len), int(k_pages), int(num_splits))
 
 
 def mla_qdecode_sparse(desc, pool, block_table, seq_lens, max_seq_len, digests, q_c, q_r, scale, k_pages, *, n_sink=1,
-                       n_recent=1, out=None, out_dtype=torch.bfloat16, lse=None, workspace=None, flags=0, stream=None):
+                       n_recent=1, out=None, out_dtype=torch.bfloat16, lse=None, num_splits=0, workspace=None, flags=0,
+                       stream=None):
     """One decode step over the pages that the digests' scores select (scores, selection, decode).
     digests may be None when k_pages covers every page. Returns (out, lse). See include/mla_qcache.h."""
     B, s_q, H, dev, pc, pr = _queries(q_c, q_r)
@@ -470,13 +471,14 @@ def mla_qdecode_sparse(desc, pool, block_table, seq_lens, max_seq_len, digests, 
     if not f32 and out.dtype is not torch.bfloat16:
         raise TypeError("out must be bfloat16 or float32")
     if workspace is None:
-        need = mla_qdecode_sparse_workspace_bytes(B, s_q, H, max_seq_len, k_pages)
+        with torch.cuda.device(dev):  # the split plan is the device's
+            need = mla_qdecode_sparse_workspace_bytes(B, s_q, H, max_seq_len, k_pages, num_splits)
         workspace = _empty((max(need, 1),), torch.uint8, dev, stream)
     nw = workspace.numel()
     _call("mla_qdecode_sparse", dev, stream, ctypes.byref(desc), _pool(desc, pool, dev), *_table(block_table, B, dev),
           _arg(seq_lens, "seq_lens", torch.int32, (B,), dev), max_seq_len,
           _opt(digests, "digests", torch.bfloat16, (desc.num_pages, D_C + D_R), dev), pc, pr, B, s_q, H, float(scale),
-          k_pages, int(n_sink), int(n_recent), _arg(workspace, "workspace", torch.uint8, (nw,), dev), nw,
+          k_pages, int(n_sink), int(n_recent), int(num_splits), _arg(workspace, "workspace", torch.uint8, (nw,), dev), nw,
           _arg(out, "out", out.dtype, (B, s_q, H, D_C), dev), f32, _opt(lse, "lse", torch.float32, (B, s_q, H), dev),
           int(flags))
     return out, lse

@@ -156,10 +156,37 @@ int page_count(int max_seq_len) { return static_cast<int>((static_cast<long>(max
 // there too: a query that sees no more than k_pages takes all of them).
 struct SparseWorkspace {
   size_t off_scores, off_table, off_lens, off_inner, inner, total;
-  int k_pages, max_keys;
+  int k_pages, max_keys, num_splits;
 };
 
-SparseWorkspace sparse_workspace(int B, int s_q, int H, int max_seq_len, int k_pages) {
+// Key splits of a decode over selections of up to max_keys keys. The general plan
+// (plan_splits) looks for full waves and leaves the combine out of account; over
+// a few thousand keys its partial sums weigh as much as a wave (256 queries of
+// 128 heads over 2,048 keys: 417 us unsplit, 472 with the general plan's two
+// splits). Model, in us: 3 a page and wave, 6 a unit's set-up and epilogue, and
+// the fp32 partials written and read at 5 TB/s behind a second launch of 3. (4
+// queries over 4,096 keys: 16 splits, as the general plan has it; 8 take 41 us
+// instead of 30.) Up to 16 rows the general plan stands.
+int sparse_splits(int queries, int H, int max_keys) {
+  if (H <= mla::kSmallRows) return 0;
+  const int pages = std::max(1, (max_keys + mla::kPage - 1) / mla::kPage);
+  const long units = static_cast<long>(queries) * ((H + 127) / 128), slots = std::max(1, device_sm_count() / 2);
+  const int n_min = (pages + kMaxChunkPages - 1) / kMaxChunkPages, n_max = std::max(n_min, std::min(pages / 4, 64));
+  int best = n_min;
+  double best_us = 1e30;
+  for (int n = n_min; n <= n_max; ++n) {
+    const double waves = static_cast<double>((units * n + slots - 1) / slots);
+    double us = waves * (3.0 * ((pages + n - 1) / n) + 6.0);
+    if (n > 1) us += 3.0 + 2.0 * n * queries * static_cast<double>(H) * mla::kDc * sizeof(float) / 5e6;
+    if (us < best_us * 0.97) {
+      best_us = us;
+      best = n;
+    }
+  }
+  return best;
+}
+
+SparseWorkspace sparse_workspace(int B, int s_q, int H, int max_seq_len, int k_pages, int num_splits) {
   const size_t queries = static_cast<size_t>(B) * s_q;
   const int width = page_count(max_seq_len);
   SparseWorkspace w{};
@@ -169,13 +196,16 @@ SparseWorkspace sparse_workspace(int B, int s_q, int H, int max_seq_len, int k_p
   w.off_table = align_up(k_pages < width ? queries * width * sizeof(float) : 0, 256);
   w.off_lens = align_up(w.off_table + queries * w.k_pages * sizeof(int32_t), 256);
   w.off_inner = align_up(w.off_lens + queries * sizeof(int32_t), 256);
-  w.inner = workspace_for(B * s_q, H, plan_splits(B * s_q, 1, H, w.max_keys, 0));
+  w.num_splits = num_splits > 0 ? num_splits : sparse_splits(B * s_q, H, w.max_keys);
+  w.inner = workspace_for(B * s_q, H, plan_splits(B * s_q, 1, H, w.max_keys, w.num_splits));
   w.total = w.off_inner + w.inner;
   return w;
 }
 
+constexpr int kMaxSelected = 1 << 20;  // pages a query may attend
+
 bool valid_selection(int k_pages, int n_sink, int n_recent) {
-  return k_pages >= 1 && k_pages <= (1 << 20) && n_sink >= 0 && n_recent >= 1 &&
+  return k_pages >= 1 && k_pages <= kMaxSelected && n_sink >= 0 && n_recent >= 1 &&
          static_cast<long>(n_sink) + n_recent <= k_pages;
 }
 
@@ -617,20 +647,20 @@ mla_status mla_select_pages(const int32_t* block_table, int max_pages_per_seq, c
   return from_cuda(mla::launch_page_select(L));
 }
 
-size_t mla_qdecode_sparse_workspace_bytes(int B, int s_q, int H, int max_seq_len, int k_pages) {
-  if (B <= 0 || s_q < 1 || H < 1 || max_seq_len < 0 || k_pages < 1) return 0;
+size_t mla_qdecode_sparse_workspace_bytes(int B, int s_q, int H, int max_seq_len, int k_pages, int num_splits) {
+  if (B <= 0 || s_q < 1 || H < 1 || max_seq_len < 0 || k_pages < 1 || k_pages > kMaxSelected || num_splits < 0) return 0;
   if (static_cast<long>(B) * s_q > 65535 || H > (1 << 20)) return 0;
-  return sparse_workspace(B, s_q, H, max_seq_len, k_pages).total;
+  return sparse_workspace(B, s_q, H, max_seq_len, k_pages, num_splits).total;
 }
 
 mla_status mla_qdecode_sparse(const mla_qcache_desc* desc, const void* pool, const int32_t* block_table,
                               int max_pages_per_seq, const int32_t* seq_lens, int max_seq_len, const void* digests,
                               const void* q_c, const void* q_r, int B, int s_q, int H, float scale, int k_pages,
-                              int n_sink, int n_recent, void* workspace, size_t workspace_bytes, void* out,
+                              int n_sink, int n_recent, int num_splits, void* workspace, size_t workspace_bytes, void* out,
                               int out_dtype, float* lse, unsigned flags, mla_stream_t stream) {
   const mla_status st = mla_qcache_check_desc(desc);
   if (st != MLA_OK) return st;
-  if (B < 0 || s_q < 1 || H < 1 || max_seq_len < 0 || !valid_selection(k_pages, n_sink, n_recent))
+  if (B < 0 || s_q < 1 || H < 1 || max_seq_len < 0 || num_splits < 0 || !valid_selection(k_pages, n_sink, n_recent))
     return MLA_ERR_INVALID_ARG;
   if (out_dtype != 0 && out_dtype != 1) return MLA_ERR_INVALID_ARG;
   if (!isfinite(scale) || (flags & ~(MLA_DECODE_FORCE_SIMT | MLA_DECODE_FAST_UNCOMPENSATED))) return MLA_ERR_INVALID_ARG;
@@ -645,7 +675,7 @@ mla_status mla_qdecode_sparse(const mla_qcache_desc* desc, const void* pool, con
       !aligned(lse, 4))
     return MLA_ERR_INVALID_ARG;
   if (static_cast<long>(max_seq_len) > static_cast<long>(max_pages_per_seq) * mla::kPage) return MLA_ERR_CAPACITY;
-  const SparseWorkspace sw = sparse_workspace(B, s_q, H, max_seq_len, k_pages);
+  const SparseWorkspace sw = sparse_workspace(B, s_q, H, max_seq_len, k_pages, num_splits);
   if (!workspace || workspace_bytes < sw.total || !aligned(workspace, 256)) return MLA_ERR_WORKSPACE;
   char* base = static_cast<char*>(workspace);
   float* scores = scored ? reinterpret_cast<float*>(base + sw.off_scores) : nullptr;
@@ -660,8 +690,8 @@ mla_status mla_qdecode_sparse(const mla_qcache_desc* desc, const void* pool, con
                        n_recent, sel_table, nullptr, sel_lens, stream);
   if (r != MLA_OK) return r;
   // B * s_q requests of one query each, over their own tables
-  DecodeCommon c{pool, desc->num_pages, sel_table, sw.k_pages, sel_lens, sw.max_keys, q_c, q_r, B * s_q, 1, H, scale, 0,
-                 sw.inner ? base + sw.off_inner : nullptr, sw.inner, out, out_dtype, lse, flags,
+  DecodeCommon c{pool, desc->num_pages, sel_table, sw.k_pages, sel_lens, sw.max_keys, q_c, q_r, B * s_q, 1, H, scale,
+                 sw.num_splits, sw.inner ? base + sw.off_inner : nullptr, sw.inner, out, out_dtype, lse, flags,
                  reinterpret_cast<cudaStream_t>(stream)};
   return run_decode(c, true, desc);
 }

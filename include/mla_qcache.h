@@ -492,13 +492,15 @@ mla_status mla_select_pages(const int32_t* block_table, int max_pages_per_seq,
                             mla_stream_t stream);
 
 /* Workspace bytes mla_qdecode_sparse needs (0 for invalid arguments). Host only. */
-size_t mla_qdecode_sparse_workspace_bytes(int B, int s_q, int H, int max_seq_len, int k_pages);
+size_t mla_qdecode_sparse_workspace_bytes(int B, int s_q, int H, int max_seq_len, int k_pages, int num_splits);
 
 /* One decode step over the selected pages: mla_page_scores, mla_select_pages
- * and mla_qdecode (library split plan) of the selection, on one stream. When
- * k_pages covers every page the scores are not computed, and H is not limited.
+ * and mla_qdecode of the selection, on one stream. When k_pages covers every
+ * page the scores are not computed, and H is not limited.
  *   digests      as for mla_page_scores (num_pages = desc's); may be NULL when
  *                k_pages >= ceil(max_seq_len / 64).
+ *   num_splits   splits of each query's selected keys, as for mla_qdecode; 0 =
+ *                library choice (its own for selections, which are short).
  *   workspace    device, 256-byte aligned, at least
  *                mla_qdecode_sparse_workspace_bytes(...) bytes; calls that may
  *                overlap need one each.
@@ -509,7 +511,7 @@ mla_status mla_qdecode_sparse(const mla_qcache_desc* desc, const void* pool,
                               const int32_t* seq_lens, int max_seq_len, const void* digests,
                               const void* q_c, const void* q_r,
                               int B, int s_q, int H, float scale,
-                              int k_pages, int n_sink, int n_recent,
+                              int k_pages, int n_sink, int n_recent, int num_splits,
                               void* workspace, size_t workspace_bytes,
                               void* out, int out_dtype, float* lse,
                               unsigned flags, mla_stream_t stream);

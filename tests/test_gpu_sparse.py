@@ -161,7 +161,7 @@ def test_select_without_scores():
     assert t.tolist() == [[[-1] * 4, [4, -1, -1, -1]]] and n.tolist() == [[0, 1]]
 
 
-def _sparse_case(fmt, lens, s_q, H, k, n_sink, n_recent, seed=0, out_dtype=torch.float32):
+def _sparse_case(fmt, lens, s_q, H, k, n_sink, n_recent, seed=0, out_dtype=torch.float32, num_splits=1):
     """The step against float64 over the pages that the library's own scores and selection name
     (each of them is tested on its own): the decode's error bound holds over the selection."""
     rng = np.random.default_rng(seed)
@@ -183,13 +183,13 @@ def _sparse_case(fmt, lens, s_q, H, k, n_sink, n_recent, seed=0, out_dtype=torch
     q_c, q_r = q[..., :512].contiguous().cuda(), q[..., 512:].contiguous().cuda()
     lse = torch.empty((B, s_q, H), device="cuda")
     out, _ = api.mla_qdecode_sparse(desc, pool_t, table_t, lens_t, L, dig, q_c, q_r, SCALE, k, n_sink=n_sink,
-                                    n_recent=n_recent, out_dtype=out_dtype, lse=lse)
+                                    n_recent=n_recent, out_dtype=out_dtype, lse=lse, num_splits=num_splits)
     scores = api.mla_page_scores(table_t, lens_t, L, dig, q_c, q_r, SCALE) if k < -(-L // 64) else None
     t, p, n = api.mla_select_pages(table_t, lens_t, L, scores, k, n_sink=n_sink, n_recent=n_recent, s_q=s_q)
     # the parts give the step's own result
     lse2 = torch.empty((B * s_q, 1, H), device="cuda")
     out2, _ = api.mla_qdecode(desc, pool_t, t.view(B * s_q, k), n.view(-1), min(64 * k, L), q_c.view(B * s_q, 1, H, 512),
-                              q_r.view(B * s_q, 1, H, 64), SCALE, out_dtype=out_dtype, lse=lse2)
+                              q_r.view(B * s_q, 1, H, 64), SCALE, out_dtype=out_dtype, lse=lse2, num_splits=num_splits)
     assert api.mla_get_device_status() == 0
     assert torch.equal(out.view(-1), out2.view(-1)) and torch.equal(lse.view(-1), lse2.view(-1))
     want = {}
@@ -219,6 +219,12 @@ def test_sparse_step(fmt, lens, s_q, H, k, n_sink, n_recent):
     _sparse_case(fmt, lens, s_q, H, k, n_sink, n_recent, seed=H + k)
 
 
+@pytest.mark.parametrize("num_splits", [2, 5])
+def test_sparse_step_split(num_splits):
+    _sparse_case((4, 64, 4, 64), [1500, 900, 20], 2, 128, 9, 1, 2, num_splits=num_splits)
+    _sparse_case((4, 64, 4, 64), [1500, 900, 20], 1, 16, 9, 1, 2, num_splits=num_splits)
+
+
 def test_sparse_step_bf16_out():
     _sparse_case((4, 64, 4, 64), [800, 90], 1, 128, 4, 1, 1, out_dtype=torch.bfloat16)
 
@@ -230,8 +236,8 @@ def test_sparse_covering_every_page_is_the_dense_decode():
     pool = torch.from_numpy(ref.random_pool(rng, fmt, pages)).cuda()
     desc = api.make_desc(*fmt, num_pages=pages)
     q_c, q_r = ref.bf16_randn(rng, (3, 1, H, 512)).cuda(), ref.bf16_randn(rng, (3, 1, H, 64)).cuda()
-    a, _ = api.mla_qdecode(desc, pool, _i32(table), _i32(lens), 300, q_c, q_r, SCALE)
-    b, _ = api.mla_qdecode_sparse(desc, pool, _i32(table), _i32(lens), 300, None, q_c, q_r, SCALE, 5)
+    a, _ = api.mla_qdecode(desc, pool, _i32(table), _i32(lens), 300, q_c, q_r, SCALE, num_splits=1)
+    b, _ = api.mla_qdecode_sparse(desc, pool, _i32(table), _i32(lens), 300, None, q_c, q_r, SCALE, 5, num_splits=1)
     assert torch.equal(a, b)
 
 

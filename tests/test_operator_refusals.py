@@ -106,7 +106,7 @@ def test_select(lib, bad, code):
 
 
 SPARSE = dict(desc=_desc(), pool=A, table=A, max_pages=4, lens=A, max_len=256, digests=A, q_c=A, q_r=A, B=2, s_q=1, H=16,
-              scale=0.1, k=3, n_sink=1, n_recent=1, ws=A, ws_bytes=1 << 24, out=A, out_dtype=0, lse=None, flags=0, stream=None)
+              scale=0.1, k=3, n_sink=1, n_recent=1, splits=0, ws=A, ws_bytes=1 << 24, out=A, out_dtype=0, lse=None, flags=0, stream=None)
 
 
 @pytest.mark.parametrize("bad,code", [
@@ -114,7 +114,7 @@ SPARSE = dict(desc=_desc(), pool=A, table=A, max_pages=4, lens=A, max_len=256, d
     (dict(table=None), INV), (dict(max_pages=0), INV), (dict(lens=None), INV), (dict(max_len=-1), INV), (dict(max_len=257), CAP),
     (dict(digests=None), INV), (dict(digests=A + 4), INV), (dict(q_c=None), INV), (dict(q_c=A + 8), INV), (dict(q_r=None), INV),
     (dict(B=-1), INV), (dict(s_q=0), INV), (dict(H=0), INV), (dict(H=129), UNS), (dict(B=65536), UNS), (dict(scale=NAN), INV),
-    (dict(k=0), INV), (dict(n_sink=3), INV), (dict(n_recent=0), INV), (dict(ws=None), WS), (dict(ws=A + 16), WS),
+    (dict(k=0), INV), (dict(n_sink=3), INV), (dict(n_recent=0), INV), (dict(splits=-1), INV), (dict(ws=None), WS), (dict(ws=A + 16), WS),
     (dict(ws_bytes=100), WS), (dict(out=None), INV), (dict(out=A + 8), INV), (dict(out_dtype=2), INV), (dict(lse=A + 2), INV),
     (dict(flags=8), INV), (dict(flags=_lib.MLA_DECODE_TEST_STALL), INV)])
 def test_sparse(lib, bad, code):
@@ -137,16 +137,24 @@ def test_empty_batches_need_nothing(lib):
 
 def test_sparse_workspace(lib):
     ws = lib.mla_qdecode_sparse_workspace_bytes
-    for bad in ((0, 1, 16, 100, 4), (2, 0, 16, 100, 4), (2, 1, 0, 100, 4), (2, 1, 16, -1, 4), (2, 1, 16, 100, 0),
-                (40000, 2, 16, 100, 4), (1, 1, (1 << 20) + 1, 100, 4)):
+    for bad in ((0, 1, 16, 100, 4, 0), (2, 0, 16, 100, 4, 0), (2, 1, 0, 100, 4, 0), (2, 1, 16, -1, 4, 0), (2, 1, 16, 100, 0, 0),
+                (40000, 2, 16, 100, 4, 0), (1, 1, (1 << 20) + 1, 100, 4, 0), (2, 1, 16, 100, 4, -1),
+                (2, 1, 16, 100, (1 << 20) + 1, 0)):
         assert ws(*bad) == 0, bad
     # scores of 128 pages a query, 6 of them selected, and the scratch of 6 requests of 384 keys
     B, s_q, H, T, k = 2, 3, 128, 8192, 6
-    inner = lib.mla_decode_workspace_bytes(B * s_q, 1, H, 64 * k, 0)
     up = lambda n: (n + 255) // 256 * 256  # noqa: E731
-    assert ws(B, s_q, H, T, k) == up(6 * 128 * 4) + up(6 * k * 4) + up(6 * 4) + inner
-    # every page selected: no scores
-    assert ws(B, s_q, H, 300, k) == up(6 * k * 4) + up(6 * 4) + lib.mla_decode_workspace_bytes(6, 1, H, 300, 0)
+    for n in (1, 2, 3):
+        inner = lib.mla_decode_workspace_bytes(B * s_q, 1, H, 64 * k, n)
+        assert ws(B, s_q, H, T, k, n) == up(6 * 128 * 4) + up(6 * k * 4) + up(6 * 4) + inner
+        # every page selected: no scores
+        assert ws(B, s_q, H, 300, k, n) == up(6 * k * 4) + up(6 * 4) + lib.mla_decode_workspace_bytes(6, 1, H, 300, n)
+    # up to 16 rows the choice is mla_qdecode's; else its own: many short selections are not split, few are
+    assert ws(B, 1, 16, T, k, 0) == up(2 * 128 * 4) + up(2 * k * 4) + up(2 * 4) + lib.mla_decode_workspace_bytes(2, 1, 16, 64 * k, 0)
+    assert ws(128, 2, 128, 32768, 32, 0) == ws(128, 2, 128, 32768, 32, 1)
+    assert ws(4, 1, 128, 131072, 64, 0) == ws(4, 1, 128, 131072, 64, 16)
+    # a selection of more than 8,192 keys is split whatever is asked for
+    assert ws(64, 1, 128, 65536, 200, 1) == ws(64, 1, 128, 65536, 200, 2)
 
 
 def test_binding_refuses_host_tensors_types_and_shapes():
