@@ -243,6 +243,14 @@ def _device_index(t, name, dtype, dims):
     return t.get_device()
 
 
+def _dense(shape):
+    strides, n = [], 1
+    for d in reversed(shape):
+        strides.append(n)
+        n *= max(d, 1)
+    return strides[::-1]
+
+
 def _empty(shape, dtype, index, stream):
     """Uninitialised tensor for a kernel on `stream` (None: the current stream): taken from that
     stream's memory, and not given back while the current stream may still read it."""
@@ -256,7 +264,7 @@ def _empty(shape, dtype, index, stream):
                 t = torch.empty(shape, dtype=dtype, device=device)
             t.record_stream(cur)
             return t
-    return torch.empty(shape, dtype=dtype, device=index)
+    return torch.empty_strided(shape, _dense(shape), dtype=dtype, device=index)
 
 
 def _call(name, index, stream, *args):
@@ -438,11 +446,9 @@ def mla_select_pages(block_table, seq_lens, max_seq_len, scores, k_pages, *, n_s
     if k_pages < 1 or s_q < 1:
         raise MlaError("mla_select_pages", _lib.MLA_ERR_INVALID_ARG)
     shape = (B, s_q, k_pages)
-    if sel_table is None and sel_pages is None:
-        sel_table, sel_pages = _empty((2, *shape), torch.int32, dev, stream).unbind(0)
-    elif sel_table is None:
+    if sel_table is None:
         sel_table = _empty(shape, torch.int32, dev, stream)
-    elif sel_pages is None:
+    if sel_pages is None:
         sel_pages = _empty(shape, torch.int32, dev, stream)
     if sel_lens is None:
         sel_lens = _empty((B, s_q), torch.int32, dev, stream)

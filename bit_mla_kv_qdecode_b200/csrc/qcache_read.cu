@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kReadThreads) qcache_read_kernel(const ReadArg
   const int64_t idx = first / kPage + blockIdx.x / kParts;  // page of the request
   // slots of the page that are asked for, and this warp's first one
   const int lo = static_cast<int>(max(first - idx * kPage, static_cast<int64_t>(0)));
-  const int hi = static_cast<int>(min(first + count - idx * kPage, static_cast<int64_t>(kPage)));
+  const int hi = static_cast<int>(max(min(first + count - idx * kPage, static_cast<int64_t>(kPage)), static_cast<int64_t>(0)));
   const int slot0 = (blockIdx.x % kParts * (kReadThreads / 32) + warp) * kTokens;
   if (slot0 >= hi || slot0 + kTokens <= lo) return;
   const int page = idx < a.max_pages ? __ldg(a.table + static_cast<size_t>(b) * a.max_pages + idx) : -1;
@@ -420,7 +420,7 @@ cudaError_t launch_read_t(const ReadLaunch& L, const ReadArgs& a) {
   // Eight tokens a warp keep four in flight for longer (ragged read of 64 requests:
   // 118 us, at two a warp 130); with few CTAs the length of each one's chain counts,
   // and two a warp finish sooner (1,021 tokens: 2.5 us instead of 4.1).
-  const unsigned pages = (L.max_rows + 62) / kPage + 1;
+  const unsigned pages = static_cast<unsigned>((static_cast<int64_t>(L.max_rows) + 62) / kPage + 1);
   if (static_cast<int64_t>(pages) * L.B < 4 * 148)
     return launch_dependent(qcache_read_kernel<BC, GC, BR, GR, 2>, dim3(4 * pages, L.B), dim3(kReadThreads), 0, L.stream, a);
   return launch_dependent(qcache_read_kernel<BC, GC, BR, GR, 8>, dim3(pages, L.B), dim3(kReadThreads), 0, L.stream, a);

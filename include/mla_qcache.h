@@ -375,7 +375,7 @@ mla_status mla_qdecode_hybrid(const mla_qcache_desc* desc, const void* pool,
  *                   elements: 512 latent channels, then 64 of the key (a column
  *                   range of a fused projection's output will do).
  *   norm_weight     device bf16 [512], or NULL (w = 1).
- *   eps             > 0, finite.
+ *   eps             > 0, finite (as the fp32 value passed).
  *   q               device bf16, head h of row r at
  *                   q + r * q_token_stride + h * q_head_stride, 64 channels; NULL
  *                   with H = 0 when there are no queries to rotate.
@@ -389,7 +389,8 @@ mla_status mla_qdecode_hybrid(const mla_qcache_desc* desc, const void* pool,
  *                   now holds for these tokens, c_hat then kr_hat, so that a
  *                   prefill attends to what later decodes will see.
  * Every pointer to bf16 and cos_sin is 16-byte aligned; strides are
- * non-negative multiples of 8 elements. A token whose angle position is outside
+ * non-negative multiples of 8 elements. Other than q_out = q, outputs overlap
+ * neither inputs nor each other. A token whose angle position is outside
  * [0, max_positions) is skipped and flagged; a cache position past the table
  * row or a table entry outside the pool skips the token's slot and its
  * rows_out row, and is flagged. B == 0 or n_new == 0 is a no-op. */
@@ -457,9 +458,10 @@ mla_status mla_page_digest(const mla_qcache_desc* desc, const void* pool,
                            void* digests, int B, mla_stream_t stream);
 
 /* Scores of the candidate pages, as above.
- *   digests      device bf16 [num_pages, 576], 16-byte aligned.
+ *   digests      device bf16 [num_pages, 576], 16-byte aligned; finite for every
+ *                candidate.
  *   block_table, max_pages_per_seq, seq_lens, max_seq_len, q_c, q_r, B, s_q, H,
- *   scale        as for mla_qdecode; H <= 128.
+ *   scale        as for mla_qdecode; H <= 128, B * s_q <= 65535.
  *   scores       device fp32 [B, s_q, W], W = ceil(max_seq_len / 64); -inf for
  *                pages that are no candidates.
  * A candidate whose table entry is outside the pool scores -inf, takes no part

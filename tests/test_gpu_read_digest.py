@@ -72,6 +72,20 @@ def test_read_parts_and_defaults():
     assert api.mla_get_device_status() == 0
 
 
+def test_read_loose_bound_and_shared_pages():
+    """The bound on a request's rows may be any int; requests may share pages."""
+    rng = np.random.default_rng(5)
+    fmt = (4, 32, 2, 64)
+    pool = torch.from_numpy(ref.random_pool(rng, fmt, 3)).cuda()
+    desc = api.make_desc(*fmt, num_pages=3)
+    out = torch.full((260, 576), 7.0, dtype=torch.bfloat16).cuda()
+    api.mla_qcache_read(desc, pool, _i32([[2, 0], [2, 1]]), _i32([0, 10]), _i32([0, 128, 246]), 2 ** 31 - 1, out[:, :512],
+                        out[:, 512:])
+    assert api.mla_get_device_status() == 0
+    assert torch.equal(out[10:64], out[128:182]) and bool((out[246:] == 7.0).all())
+    assert not bool((out[:246] == 7.0).all(1).any())
+
+
 def test_read_bad_data_is_skipped():
     rng = np.random.default_rng(4)
     fmt = (2, 64, 2, 32)
@@ -162,6 +176,17 @@ def test_digest_many_pages_with_bad_ones():
     api.mla_page_digest(desc, pool, _i32([[25]]), _i32([0]), 64, alone)
     assert api.mla_get_device_status() == 0
     assert torch.equal(out, alone)
+
+
+def test_digest_of_a_page_two_requests_share():
+    rng = np.random.default_rng(5)
+    fmt = (2, 32, 4, 64)
+    pool = torch.from_numpy(ref.random_pool(rng, fmt, 3)).cuda()
+    desc = api.make_desc(*fmt, num_pages=3)
+    a, b = api.new_digests(desc), api.new_digests(desc)
+    api.mla_page_digest(desc, pool, _i32([[2, 0], [2, 1]]), _i32([0, 0]), 128, a)
+    api.mla_page_digest(desc, pool, _i32([[0, 1, 2]]), _i32([0]), 192, b)
+    assert torch.equal(a, b) and api.mla_get_device_status() == 0
 
 
 def test_digest_bad_data_is_skipped():

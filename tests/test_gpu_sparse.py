@@ -361,3 +361,75 @@ def test_step_captured_in_a_graph_and_on_another_stream():
     side.synchronize()
     assert torch.equal(got, want[0])
     assert api.mla_get_device_status() == 0
+
+
+def test_steps_at_once_on_two_streams():
+    """Two batches' steps in flight together, each with its own workspace, give what they give alone."""
+    rng = np.random.default_rng(21)
+    fmt, H, k = (4, 64, 4, 64), 128, 6
+    jobs = []
+    for lens in ([4000, 300, 2500], [1800, 3900, 64, 1]):
+        lens = np.array(lens)
+        table, pages = ref.random_table(rng, lens)
+        desc = api.make_desc(*fmt, num_pages=pages)
+        pool, dig = torch.from_numpy(ref.random_pool(rng, fmt, pages)).cuda(), api.new_digests(desc)
+        api.mla_page_digest(desc, pool, _i32(table), torch.zeros(len(lens), dtype=torch.int32).cuda(), int(lens.max()), dig,
+                            new_lens=_i32(lens))
+        q_c, q_r = ref.bf16_randn(rng, (len(lens), 1, H, 512)).cuda(), ref.bf16_randn(rng, (len(lens), 1, H, 64)).cuda()
+        jobs.append((desc, pool, _i32(table), _i32(lens), int(lens.max()), dig, q_c, q_r, SCALE, k))
+    alone = [api.mla_qdecode_sparse(*j)[0] for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        outs = [api.mla_qdecode_sparse(*j, stream=s)[0] for j, s in zip(jobs, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(alone, outs))
+    assert api.mla_get_device_status() == 0
+
+
+def test_two_graphs_take_turns():
+    """Two captured steps of different batches, replayed alternately and with new inputs."""
+    rng = np.random.default_rng(22)
+    fmt, H, k = (2, 32, 4, 64), 16, 4
+    graphs = []
+    for lens in ([2000, 130], [900, 700, 5]):
+        lens = np.array(lens)
+        table, pages = ref.random_table(rng, lens + 64)
+        desc = api.make_desc(*fmt, num_pages=pages)
+        pool, dig = torch.from_numpy(ref.random_pool(rng, fmt, pages)).cuda(), api.new_digests(desc)
+        lens_t, L = _i32(lens), int(lens.max()) + 64
+        api.mla_page_digest(desc, pool, _i32(table), torch.zeros_like(lens_t), L, dig, new_lens=lens_t)
+        q = ref.bf16_randn(rng, (len(lens), 1, H, 576)).cuda()
+        q_c, q_r = q[..., :512].contiguous(), q[..., 512:].contiguous()
+        args = (desc, pool, _i32(table), lens_t, L, dig, q_c, q_r, SCALE, k)
+        api.mla_qdecode_sparse(*args)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = api.mla_qdecode_sparse(*args)[0]
+        graphs.append((g, out, args, q_c, lens_t))
+    for step in range(3):
+        for g, _, _, _, _ in graphs:
+            g.replay()
+        for g, out, args, q_c, lens_t in graphs:
+            assert torch.equal(out, api.mla_qdecode_sparse(*args)[0]), step
+            q_c.copy_(torch.flip(q_c, [0]))
+            lens_t += 7
+    assert api.mla_get_device_status() == 0
+
+
+def test_batches_of_nothing():
+    desc = api.make_desc(4, 64, 4, 64, num_pages=1)
+    pool, dig = api.new_qcache_pool(desc), api.new_digests(desc)
+    for B, L in ((0, 100), (2, 64), (2, 0)):
+        table = torch.zeros((B, 2), dtype=torch.int32, device="cuda")
+        lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+        q_c = torch.ones((B, 1, 4, 512), dtype=torch.bfloat16, device="cuda")
+        q_r = torch.ones((B, 1, 4, 64), dtype=torch.bfloat16, device="cuda")
+        lse = torch.zeros((B, 1, 4), device="cuda")
+        out, _ = api.mla_qdecode_sparse(desc, pool, table, lens, L, dig, q_c, q_r, SCALE, 1, n_sink=0, lse=lse)
+        assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+        sc = api.mla_page_scores(table, lens, L, dig, q_c, q_r, SCALE)
+        assert sc.shape == (B, 1, -(-L // 64)) and bool(torch.isneginf(sc).all())
+        t, p, n = api.mla_select_pages(table, lens, L, sc, 1, n_sink=0)
+        assert bool((t == -1).all()) and bool((p == -1).all()) and bool((n == 0).all())
+    assert api.mla_get_device_status() == 0
