@@ -291,13 +291,14 @@ __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArg
   float top = -CUDART_INF_F, sum = 0.0f;  // this lane's head over the warp's pages
   float refs[kHeld][4] = {};              // of the held tiles: what each 16 columns' exponents are relative to
 
-  // 16 columns of a tile's logits, in powers of two: the three accumulators' sum, scaled.
-  auto add_up = [&](int buf, int c, float (&v)[16]) {
-    uint32_t r[kAccs][16];
+  // 16 columns of a tile's logits, in powers of two: the three accumulators,
+  // fetched, and their sum, scaled.
+  auto fetch = [&](int buf, int c, uint32_t (&r)[kAccs][16]) {
     ptx::tmem_ld16(my_cols + buf * kTile + c, r[0]);
     ptx::tmem_ld16(my_cols + kScratchCol + c, r[1]);
     ptx::tmem_ld16(my_cols + kScratchCol + kTile + c, r[2]);
-    ptx::tmem_ld_wait();
+  };
+  auto add_up = [&](const uint32_t (&r)[kAccs][16], float (&v)[16]) {
 #pragma unroll
     for (int k = 0; k < 16; ++k)
       v[k] = (__uint_as_float(r[0][k]) + __uint_as_float(r[1][k]) + __uint_as_float(r[2][k])) * a.scale_log2;
@@ -324,11 +325,15 @@ __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArg
       if (!warp_wait(&m.t_full[buf], (n / kHeld) & 1)) break;
       ptx::tc_fence_after();
       if (heads) {
+        uint32_t r[kAccs][16];
+        fetch(buf, 0, r);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int c = 16 * q;
           float v[16];
-          add_up(buf, c, v);
+          ptx::tmem_ld_wait();
+          add_up(r, v);
+          if (q < 3) fetch(buf, c + 16, r);  // on its way while these columns are worked on
           const uint32_t mask = (q < 2 ? ok0 : ok1) >> (c & 16) & 0xffffu;
           if (mask != 0xffffu) {
 #pragma unroll
@@ -413,22 +418,28 @@ __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArg
           ptx::tc_fence_after();
         }
         if (heads && have) {
+          uint32_t held[kTwice ? 1 : 4][16];
+          if (!kTwice) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ptx::tmem_ld16(my_cols + buf * kTile + 16 * q, held[kTwice ? 0 : q]);
+            ptx::tmem_ld_wait();
+          }
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int c = 16 * q;
             float v[16], f;
             if (kTwice) {
-              add_up(buf, c, v);
+              uint32_t r[kAccs][16];
+              fetch(buf, c, r);
+              ptx::tmem_ld_wait();
+              add_up(r, v);
               f = inv;
 #pragma unroll
               for (int e = 0; e < 16; ++e) v[e] = exp2_approx(v[e] - top);
             } else {
-              uint32_t r[16];
-              ptx::tmem_ld16(my_cols + buf * kTile + c, r);
-              ptx::tmem_ld_wait();
               f = exp2_approx((n == 0 ? refs[0][q] : refs[1][q]) - top) * inv;
 #pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(r[e]);
+              for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(held[kTwice ? 0 : q][e]);
             }
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = h < a.H ? v[e] * f : 0.0f;
@@ -504,12 +515,50 @@ bool make_rows_map(CUtensorMap* m, const void* base, int width, int64_t n, int r
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Clusters of 1, 2, 4 and 8 CTAs that run at once on the current device (one CTA
+// an SM; clusters stay within a GPC, whose SMs they need not fill). Asked once a device.
+constexpr int kMaxDevices = 64, kSizes = 4;
+static_assert(1 << (kSizes - 1) == kMaxCluster, "cluster sizes");
+std::mutex g_slots_mu;
+int g_slots[kMaxDevices][kSizes];
+
+cudaError_t cluster_slots(int (&slots)[kSizes]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(g_slots_mu);
+  int* kept = g_slots[dev];
+  if (kept[0] == 0) {
+    for (auto kern : {page_scores_kernel<false>, page_scores_kernel<true>}) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+      if (e != cudaSuccess) return e;
+    }
+    int got[kSizes];
+    for (int i = 0; i < kSizes; ++i) {
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(1u << i);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = kSmemLimit;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim = {1u << i, 1, 1};
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&got[i], page_scores_kernel<false>, &cfg);
+      if (e != cudaSuccess) return e;
+    }
+    for (int i = kSizes - 1; i >= 0; --i) kept[i] = std::max(got[i], i == 0 ? 1 : 0);
+  }
+  for (int i = 0; i < kSizes; ++i) slots[i] = kept[i];
+  return cudaSuccess;
+}
+
 }  // namespace
 
 cudaError_t launch_page_scores(const PageScoresLaunch& L) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int slots[kSizes];
+  const cudaError_t e = cluster_slots(slots);
   if (e != cudaSuccess) return e;
   const int q_block = (L.H + 7) / 8 * 1024;
   const int stages = std::min((kSmemLimit - kSmemFixed - kBlocks * q_block) / kStageBytes, kMaxStages);
@@ -526,9 +575,10 @@ cudaError_t launch_page_scores(const PageScoresLaunch& L) {
   const int tiles = (L.width + kTile - 1) / kTile;
   int best = 1;
   double best_cost = 1e30;
-  for (int c = 1; c <= kMaxCluster; c *= 2) {
-    const int per = (tiles + c - 1) / c;
-    const int64_t waves = (units * c + sms - 1) / sms;
+  for (int i = 0; i < kSizes; ++i) {
+    if (slots[i] == 0) continue;
+    const int c = 1 << i, per = (tiles + c - 1) / c;
+    const int64_t waves = (units + slots[i] - 1) / slots[i];
     const double cost = waves * (per * (per > kHeld ? 2.0 : 1.0) + L.H / 128.0 + 0.5);
     if (cost < best_cost * 0.97) {
       best_cost = cost;
@@ -536,8 +586,6 @@ cudaError_t launch_page_scores(const PageScoresLaunch& L) {
     }
   }
   auto kern = (tiles + best - 1) / best > kHeld ? page_scores_kernel<true> : page_scores_kernel<false>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(units * best));
   cfg.blockDim = dim3(kThreads);
