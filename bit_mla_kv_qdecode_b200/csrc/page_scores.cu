@@ -11,7 +11,7 @@
 // CTAs) the statistics of the whole query are known before any logit is read
 // again, and none goes through memory. A longer query's tiles are computed
 // twice, first for the statistics. (Pages as the M side, with the statistics
-// reduced across lanes, took 3.7 us a tile of 128 heads instead of 0.5.)
+// reduced across lanes, took 3.7 us a tile of 128 heads for them instead of 1.1.)
 //
 // Precision. The tensor cores' fp32 accumulation truncates, in proportion to
 // the sum so far and to the steps: with one accumulator for all 576 channels
@@ -23,17 +23,17 @@
 // Digests are gathered by the block table with 16-byte asynchronous copies into
 // the swizzled operand layout, 64 channels of 128 pages a stage; the query's
 // heads come with nine tiled loads and stay for all tiles. (TMA's gather of four
-// rows a request moved 10 GB/s an SM at 128 bytes a row, these copies 43.)
+// rows a request moved 10 GB/s an SM at 128 bytes a row, these copies 38 with the
+// four stages that 128 heads leave room for, 48 where HBM is the limit.)
 // Warp roles:
 //   warps 0-7   a quarter of the heads and half of a tile's pages each:
 //               statistics, later weights and their sum over the heads
-//   warps 8-15  copies (four warps reached 42 GB/s, eight 70)
-//   warps 16-18 MMA issue, one accumulator each (a stage costs its issuing
+//   warps 8-11  copies (eight were 2 % slower: fewer registers for the others)
+//   warps 12-14 MMA issue, one accumulator each (a stage costs its issuing
 //               thread 380 ns of waits and issue, its MMAs 130); tensor memory
 // The CTAs' statistics meet in distributed shared memory, in rank order, so
 // results do not depend on timing. Every wait is bounded; one that runs out
 // sets MLA_ERR_TIMEOUT and leaves the scores undefined.
-#include <cuda.h>
 #include <math_constants.h>
 
 #include <algorithm>
@@ -42,17 +42,19 @@
 #include "mla_common.cuh"
 #include "mla_internal.h"
 #include "sm100_ptx.cuh"
+#include "tensor_map.h"
 
 namespace mla {
 namespace {
 
-constexpr int kSoftWarps = 8, kCopyWarps = 8;
+constexpr int kSoftWarps = 8, kCopyWarps = 4;
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kMaxCluster = 8;
 constexpr int kAccs = 3;                           // accumulators of a logit, a warp that issues for each
 constexpr int kMmaWarp = kSoftWarps + kCopyWarps;  // the first of them
 constexpr int kThreads = (kMmaWarp + kAccs) * 32;
 constexpr int kTile = 128;                         // pages of a tile
+constexpr int kCopyPages = kTile / kCopyWarps;     // of them a copying warp takes
 constexpr int kBlockCh = 64;                       // channels of one operand stage (128 B a row)
 constexpr int kBlocks = kDqk / kBlockCh;           // 9: eight of the content, one of the RoPE part
 constexpr int kStageBytes = kTile * kBlockCh * 2;  // 16 KB
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArg
   ptx::griddep_wait();
 
   // the copying warps' first table entries come along with the length
-  const int copy_page = 16 * (warp - kSoftWarps) + (lane & 15);  // of a tile: the page this lane looks up
+  const int copy_page = kCopyPages * (warp - kSoftWarps) + lane % kCopyPages;  // of a tile: the page this lane looks up
   auto table_at = [&](int p) { return p < a.max_pages ? __ldg(a.table + static_cast<size_t>(b) * a.max_pages + p) : -1; };
   int entry = -1;
   if (warp >= kSoftWarps && warp < kMmaWarp) entry = table_at(rank * kTile + copy_page);
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArg
   auto tile_of = [&](int n) { return rank + (n < mine ? n : n - mine) * C; };  // n counts over both sweeps
 
   // Copy the digests of this CTA's tiles into the ring. Eight lanes take one
-  // page's 128 bytes of a stage, a warp 16 pages. `entry` is the lane's table
+  // page's 128 bytes of a stage, a warp kCopyPages pages. `entry` is the lane's table
   // entry of the next tile.
   auto produce = [&](int n0, int n1) {
     const int w = warp - kSoftWarps, sub = lane >> 3, chunk = lane & 7;
@@ -232,9 +234,9 @@ __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArg
       // pages that are none read page 0; their logits are masked
       const bool ok = tile_of(n) * kTile + copy_page < P && page_valid(entry, a.num_pages);
       const int mine_page = ok ? entry : 0;
-      const uint8_t* src[4];
+      const uint8_t* src[kCopyPages / 4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kCopyPages / 4; ++j) {
         const int page = __shfl_sync(0xffffffffu, mine_page, 4 * j + sub);
         src[j] = reinterpret_cast<const uint8_t*>(a.digests + static_cast<size_t>(page) * kDqk) + 16 * chunk;
       }
@@ -242,9 +244,9 @@ __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArg
       for (int k = 0; k < kBlocks; ++k) {
         const int it = n * kBlocks + k, round = it / a.stages, s = it - round * a.stages;
         if (round > 0 && !warp_wait(&m.empty[s], (round - 1) & 1)) return;
-        const uint32_t dst = ptx::smem_u32(ring + s * kStageBytes) + 16 * w * 128;
+        const uint32_t dst = ptx::smem_u32(ring + s * kStageBytes) + kCopyPages * w * 128;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kCopyPages / 4; ++j) {
           const int r = 4 * j + sub;
           cp_async16(dst + r * 128 + ((chunk ^ (r & 7)) << 4), src[j] + k * (kBlockCh * 2));
         }
@@ -485,34 +487,12 @@ __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArg
 
 // ---------------------------------------------------------------- host side
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
-
-// Rows of `width` bf16 channels, in boxes of 64 channels x `rows`, 128-byte swizzle.
+// Rows of `width` bf16 channels, in boxes of 64 channels x `rows`.
 bool make_rows_map(CUtensorMap* m, const void* base, int width, int64_t n, int rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(n)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(width) * 2};
   const cuuint32_t box[2] = {kBlockCh, static_cast<cuuint32_t>(rows)};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_swizzled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 2, dims, strides, box);
 }
 
 // Clusters of 1, 2, 4 and 8 CTAs that run at once on the current device (one CTA

@@ -12,6 +12,7 @@
 #include "mla_common.cuh"
 #include "mla_internal.h"
 #include "sm100_ptx.cuh"
+#include "tensor_map.h"
 
 namespace mla {
 namespace {
@@ -186,47 +187,47 @@ struct DigestArgs {
 
 // The sums on warp-level MMAs: sum_t u_t s_t over a page's 64 tokens is a product
 // of the steps (one row for each group of channels) with the codes (tokens x
-// channels), both exact in fp16, accumulated in fp32. Two tokens' codes become a
-// pair of fp16 values in place, by setting them into the low bits of 1024 and
-// subtracting it, 1.6 instructions a value with all loads (fp32 multiply-adds on
-// the vector unit took 4.5: 19.3 us for the 2,048 pages of a prefill, bound by
-// their issue). Nine warps, each with 64 channels of its own and no exchange.
+// channels), accumulated in fp32. A code standing alone in the low ten bits of an
+// fp16 value is the subnormal u * 2^(place - 24), exact, and so are its products:
+// one mask makes a pair of operands out of two tokens' codes, and the sum takes
+// back the power of two. (fp32 multiply-adds on the vector unit were bound by
+// their issue, 4.5 instructions a value.) Nine warps, each with 64 channels of
+// its own and no exchange.
 constexpr int kDigestWarps = 9;  // eight of the content, one of the RoPE part
 constexpr int kDigestThreads = 32 * kDigestWarps;
 
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-// c[16 x 8] += a[16 x 16] b[16 x 8], rows 8-15 of a zero (and so c[2] and c[3]).
+// c[16 x 8] += a[16 x 16] b[16 x 8], rows 8-15 of a zero (and so c[2] and c[3]). A
+// row of c that is not read may come of any row of a.
 __device__ __forceinline__ void mma_steps(float (&c)[4], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(0u), "r"(a2), "r"(0u), "r"(b0), "r"(b1));
 }
 
+// Where a page part's codes are: in global memory; in shared memory; in shared
+// memory in boxes of 64 rows x 128 bytes with the 128-byte swizzle.
+enum class At { kGlobal, kShared, kSwizzled };
+
 // Mean over a page's tokens of the 64 channels from 64 * part on, of codes of BITS
 // in rows of CHANNELS with groups of G; out: their bf16 values.
-template <int BITS, int CHANNELS, int G, bool kShared>
+template <int BITS, int CHANNELS, int G, At kAt>
 __device__ __forceinline__ void mean_of_tokens(const uint8_t* codes, const uint8_t* metas, int part, __nv_bfloat16* out,
                                                int lane) {
   constexpr int kRow = CHANNELS * BITS / 8, kGroups = CHANNELS / G, kMine = 64 / G;  // groups of the warp: 1 or 2
   const int q = lane & 3, r = lane >> 2;
   auto load_meta = [&](int t, int g) -> uint32_t {
     const uint32_t* p = reinterpret_cast<const uint32_t*>(metas) + t * kGroups + kMine * part + g;
-    return kShared ? *p : __ldg(p);
+    return kAt == At::kGlobal ? __ldg(p) : *p;
   };
   // eight codes of token t, unit r of the warp's channels
   auto load_unit = [&](int t) -> uint32_t {
-    if constexpr (BITS == 4) {
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(codes + t * kRow) + 8 * part + r;
-      return kShared ? *p : __ldg(p);
-    } else {
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(codes + t * kRow) + 8 * part + r;
-      return kShared ? *p : __ldg(p);
-    }
+    const int byte = BITS * (8 * part + r);  // in the token's row
+    const uint8_t* p = codes + t * kRow + byte;
+    if (kAt == At::kSwizzled) p = codes + byte / 128 * (kPage * 128) + t * 128 + (((byte / 16 ^ t) & 7) << 4) + byte % 16;
+    if constexpr (BITS == 4)
+      return kAt == At::kGlobal ? __ldg(reinterpret_cast<const uint32_t*>(p)) : *reinterpret_cast<const uint32_t*>(p);
+    else
+      return kAt == At::kGlobal ? __ldg(reinterpret_cast<const uint16_t*>(p)) : *reinterpret_cast<const uint16_t*>(p);
   };
   uint32_t w[4][4], m[4][4];  // K-step, token 2q + {0, 1, 8, 9} of it
 #pragma unroll
@@ -235,7 +236,7 @@ __device__ __forceinline__ void mean_of_tokens(const uint8_t* codes, const uint8
     for (int e = 0; e < 4; ++e) {
       const int t = 16 * k + 2 * q + (e & 1) + 8 * (e >> 1);
       w[k][e] = load_unit(t);
-      m[k][e] = r < kMine ? load_meta(t, r) : 0u;
+      m[k][e] = load_meta(t, r % kMine);  // rows of the other lanes are not read
     }
   float z[kMine];  // offsets, over the tokens
 #pragma unroll
@@ -255,9 +256,7 @@ __device__ __forceinline__ void mean_of_tokens(const uint8_t* codes, const uint8
       for (int j = 0; j < kCodes; ++j) {
         const int down = j < kInPlace ? 0 : kInPlace * BITS;
         const uint32_t mask = ((1u << BITS) - 1) * 0x00010001u << (j * BITS - down);
-        const uint32_t b0 = hadd2((p0 >> down & mask) | 0x64006400u, 0xE400E400u);  // 1024 + ..., less 1024
-        const uint32_t b1 = hadd2((p1 >> down & mask) | 0x64006400u, 0xE400E400u);
-        mma_steps(acc[half * kCodes + j], a0, a2, b0, b1);
+        mma_steps(acc[half * kCodes + j], a0, a2, p0 >> down & mask, p1 >> down & mask);
       }
     }
   }
@@ -277,8 +276,8 @@ __device__ __forceinline__ void mean_of_tokens(const uint8_t* codes, const uint8
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         constexpr int kCodes = 16 / BITS, kInPlace = BITS == 4 ? 2 : 5;
-        const int c = (j + i) % kCodes, place = c < kInPlace ? c : c - kInPlace;  // the value stood 2^(BITS place) too high
-        v[i] = fmaf(acc[j + i][e], 1.0f / (1 << (BITS * place)), zr) * (1.0f / kPage);
+        const int c = (j + i) % kCodes, place = c < kInPlace ? c : c - kInPlace;
+        v[i] = fmaf(acc[j + i][e], static_cast<float>(1 << (24 - BITS * place)), zr) * (1.0f / kPage);
       }
       const __nv_bfloat162 h = __floats2bfloat162_rn(v[0], v[1]);
       o[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
@@ -303,14 +302,18 @@ __device__ __forceinline__ int completed_page(const DigestArgs& a, int b, int x)
   return page;
 }
 
-// One warp's share of a page's digest.
+// One warp's share of a page's digest: content codes at `content`, the rest of the
+// page (from its RoPE codes on) at `rest`.
 template <int BC, int GC, int BR, int GR, bool kShared>
-__device__ __forceinline__ void digest_warp(const uint8_t* pg, __nv_bfloat16* row, int warp, int lane) {
+__device__ __forceinline__ void digest_warp(const uint8_t* content, const uint8_t* rest, __nv_bfloat16* row, int warp,
+                                            int lane) {
   using G = QGeom<BC, GC, BR, GR>;
   if (warp < 8)
-    mean_of_tokens<BC, kDc, GC, kShared>(pg + G::kOffCC, pg + G::kOffCM, warp, row, lane);
+    mean_of_tokens<BC, kDc, GC, kShared ? At::kSwizzled : At::kGlobal>(content, rest + (G::kOffCM - G::kOffRC), warp, row,
+                                                                      lane);
   else
-    mean_of_tokens<BR, kDr, GR, kShared>(pg + G::kOffRC, pg + G::kOffRM, 0, row + kDc, lane);
+    mean_of_tokens<BR, kDr, GR, kShared ? At::kShared : At::kGlobal>(rest, rest + (G::kOffRM - G::kOffRC), 0, row + kDc,
+                                                                    lane);
 }
 
 // Few pages (a decode step): one CTA for each that may be complete.
@@ -320,32 +323,40 @@ __global__ void __launch_bounds__(kDigestThreads) page_digest_kernel(const Diges
   ptx::griddep_launch_dependents();
   const int page = completed_page(a, blockIdx.y, blockIdx.x);
   if (page < 0) return;
-  digest_warp<BC, GC, BR, GR, false>(a.pool + static_cast<size_t>(page) * QGeom<BC, GC, BR, GR>::kPageBytes,
-                                     a.digests + static_cast<size_t>(page) * kDqk, threadIdx.x >> 5, threadIdx.x & 31);
+  using G = QGeom<BC, GC, BR, GR>;
+  const uint8_t* pg = a.pool + static_cast<size_t>(page) * G::kPageBytes;
+  digest_warp<BC, GC, BR, GR, false>(pg + G::kOffCC, pg + G::kOffRC, a.digests + static_cast<size_t>(page) * kDqk,
+                                     threadIdx.x >> 5, threadIdx.x & 31);
 }
 
-// Many pages (after a prefill): two CTAs an SM walk the pages, one warp looking up
-// 32 of them at a time and copying each whole page (it is contiguous) into a
-// ring, nine warps summing from there. A CTA a page spends most of its time in
-// three dependent round trips to memory. Bound: bytes (14,592-24,832 read, 1,152
-// written a page).
+// Many pages (after a prefill): CTAs walk the pages, one warp looking up 32 of
+// them at a time and copying each whole into a ring, nine warps summing from
+// there. The content codes come as TMA boxes in the 128-byte swizzle: a warp's
+// fragment takes 32 bytes from each of four tokens, whose rows would otherwise
+// share their banks (or, read from global memory directly, take four lines a load).
+// Bound: instructions (2,048 pages: 14.1 us; the copies alone 8.6, the sums alone
+// about 12; bytes, 14,592-24,832 read and 1,152 written a page, 6.8).
 constexpr int kRingPages = 4, kRingCtas = 2;
 constexpr uint64_t kRingWaitNs = 2000000000ull;
 
-template <int kPageBytes>
+template <int kContent, int kRest>
 struct DigestRing {
-  alignas(128) uint8_t pages[kRingPages][(kPageBytes + 127) / 128 * 128];
+  struct alignas(1024) Stage {
+    uint8_t content[kContent], rest[kRest];
+  } stages[kRingPages];
   uint64_t full[kRingPages], empty[kRingPages];
   int page[kRingPages];
   int abort;
 };
 
 template <int BC, int GC, int BR, int GR>
-__global__ void __launch_bounds__(kDigestThreads + 32, kRingCtas) page_digest_ring_kernel(const DigestArgs a, int per_request,
-                                                                                 int items) {
-  constexpr int kPageBytes = QGeom<BC, GC, BR, GR>::kPageBytes;
-  extern __shared__ __align__(128) uint8_t smem_raw[];
-  DigestRing<kPageBytes>& m = *reinterpret_cast<DigestRing<kPageBytes>*>(smem_raw);
+using RingOf = DigestRing<QGeom<BC, GC, BR, GR>::kOffRC, QGeom<BC, GC, BR, GR>::kPageBytes - QGeom<BC, GC, BR, GR>::kOffRC>;
+
+template <int BC, int GC, int BR, int GR>
+__global__ void __launch_bounds__(kDigestThreads + 32, kRingCtas) page_digest_ring_kernel(const DigestArgs a, const __grid_constant__ CUtensorMap codes, int per_request, int items) {
+  using G = QGeom<BC, GC, BR, GR>;
+  extern __shared__ uint8_t smem_raw[];
+  auto& m = *reinterpret_cast<RingOf<BC, GC, BR, GR>*>(smem_raw + ((1024 - (ptx::smem_u32(smem_raw) & 1023)) & 1023));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kRingPages; ++s) {
@@ -385,8 +396,12 @@ __global__ void __launch_bounds__(kDigestThreads + 32, kRingCtas) page_digest_ri
         const int s = next_slot();
         if (ok && lane == 0) {
           m.page[s] = page;
-          ptx::mbar_arrive_expect_tx(&m.full[s], kPageBytes);
-          ptx::bulk_load(m.pages[s], a.pool + static_cast<size_t>(page) * kPageBytes, kPageBytes, &m.full[s]);
+          ptx::mbar_arrive_expect_tx(&m.full[s], G::kPageBytes);
+#pragma unroll
+          for (int x = 0; x < G::kRowC; x += 128)
+            ptx::tma_load_3d(m.stages[s].content + x * kPage, &codes, x, 0, page, &m.full[s]);
+          ptx::bulk_load(m.stages[s].rest, a.pool + static_cast<size_t>(page) * G::kPageBytes + G::kOffRC,
+                         G::kPageBytes - G::kOffRC, &m.full[s]);
         }
       }
     }
@@ -409,7 +424,8 @@ __global__ void __launch_bounds__(kDigestThreads + 32, kRingCtas) page_digest_ri
     if (!wait(&m.full[s], (it / kRingPages) & 1)) break;
     const int page = m.page[s];
     if (page < 0) break;
-    digest_warp<BC, GC, BR, GR, true>(m.pages[s], a.digests + static_cast<size_t>(page) * kDqk, warp, lane);
+    digest_warp<BC, GC, BR, GR, true>(m.stages[s].content, m.stages[s].rest, a.digests + static_cast<size_t>(page) * kDqk,
+                                      warp, lane);
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&m.empty[s]);
   }
@@ -417,9 +433,10 @@ __global__ void __launch_bounds__(kDigestThreads + 32, kRingCtas) page_digest_ri
 
 template <int BC, int GC, int BR, int GR>
 cudaError_t launch_read_t(const ReadLaunch& L, const ReadArgs& a) {
-  // Eight tokens a warp keep four in flight for longer (ragged read of 64 requests:
-  // 118 us, at two a warp 130); with few CTAs the length of each one's chain counts,
-  // and two a warp finish sooner (1,021 tokens: 2.5 us instead of 4.1).
+  // Eight tokens a warp keep four in flight for longer (64 requests of up to 16,384
+  // tokens: 97 us, at two a warp 114); with few CTAs the length of each one's chain
+  // counts, and two a warp finish sooner (1,021 tokens: 2.0 us instead of 3.4; even
+  // at 32,768 tokens).
   const unsigned pages = static_cast<unsigned>((static_cast<int64_t>(L.max_rows) + 62) / kPage + 1);
   if (static_cast<int64_t>(pages) * L.B < 4 * 148)
     return launch_dependent(qcache_read_kernel<BC, GC, BR, GR, 2>, dim3(4 * pages, L.B), dim3(kReadThreads), 0, L.stream, a);
@@ -430,17 +447,26 @@ template <int BC, int GC, int BR, int GR>
 cudaError_t launch_digest_t(const DigestLaunch& L, const DigestArgs& a) {
   const int per_request = L.n_new / kPage + 1;
   const int64_t items = static_cast<int64_t>(per_request) * L.B;
-  if (items < 4 * 148 || items > 0x7fffffff)
+  // A CTA a page is as fast up to about a thousand pages, four to an SM twice over (16
+  // requests of 64 pages: 7.8 us, the ring 8.1; 32: 16.9 and 14.1; two pages of
+  // 128 requests: 2.5 and 3.0).
+  if (items < 8 * 148 || items > 0x7fffffff || L.num_pages < 1)
     return launch_dependent(page_digest_kernel<BC, GC, BR, GR>, dim3(per_request, L.B), dim3(kDigestThreads), 0, L.stream, a);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   auto kern = page_digest_ring_kernel<BC, GC, BR, GR>;
-  constexpr int kSmem = sizeof(DigestRing<QGeom<BC, GC, BR, GR>::kPageBytes>);
+  constexpr int kSmem = sizeof(RingOf<BC, GC, BR, GR>) + 1024;
   static_assert(kRingCtas * (kSmem + 1024) <= 233472, "CTAs an SM");
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kern, dim3(kRingCtas * sms), dim3(kDigestThreads + 32), kSmem, L.stream, a, per_request,
+  using G = QGeom<BC, GC, BR, GR>;
+  CUtensorMap codes;
+  const cuuint64_t dims[3] = {G::kRowC, kPage, static_cast<cuuint64_t>(L.num_pages)}, strides[2] = {G::kRowC, G::kPageBytes};
+  const cuuint32_t box[3] = {128, kPage, 1};
+  if (!encode_swizzled(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<const uint8_t*>(L.pool) + G::kOffCC, 3, dims, strides, box))
+    return cudaErrorInvalidValue;
+  return launch_dependent(kern, dim3(kRingCtas * sms), dim3(kDigestThreads + 32), kSmem, L.stream, a, codes, per_request,
                           static_cast<int>(items));
 }
 
