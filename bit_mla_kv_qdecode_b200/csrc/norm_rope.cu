@@ -15,7 +15,10 @@
 // practice. The queries meet no border and are rotated in fp32.
 //
 // Bound: bytes. A token reads 1,152 B and writes its 228-388 B slot (and 1,152 B
-// of rows when asked); its queries read and write 128 B a head each.
+// of rows when asked); its queries read and write 128 B a head each. 8,192 tokens
+// of 128 heads (padded): 45.4 us, 5.8 TB/s; with the tokens' blocks ahead of the
+// queries' instead of among them 50.6, with 16 heads a warp instead of 32 52.5.
+// A step of 32 tokens is latency, 5.2 us.
 #include "append_token.cuh"
 #include "mla_common.cuh"
 #include "mla_internal.h"
@@ -44,7 +47,7 @@ struct NormRopeArgs {
   __nv_bfloat16* rows_out;
   int* status;
   double eps;
-  int num_pages, max_pages, max_positions, n_tokens, n_new, H, head_chunks, token_blocks;
+  int num_pages, max_pages, max_positions, n_tokens, n_new, H, head_chunks, token_blocks, period;
 };
 
 // Position whose angle token `tok` (token j of request b) is turned by, or -1
@@ -204,11 +207,14 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_append_kernel(const Nor
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (static_cast<int>(blockIdx.x) < a.token_blocks) {
-    const int tok = blockIdx.x * kWarps + warp;
+  // every period-th block takes eight tokens, the others eight units of queries: the
+  // tokens' long chains (look-up, fp64 norm, quantizer) run beside the queries' traffic
+  const int t = blockIdx.x / a.period;
+  if (blockIdx.x % a.period == 0 && t < a.token_blocks) {
+    const int tok = t * kWarps + warp;
     if (tok < a.n_tokens) token_warp<BC, GC, BR, GR, kHalf>(a, tok, lane);
   } else {
-    const int64_t unit = static_cast<int64_t>(blockIdx.x - a.token_blocks) * kWarps + warp;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x - min(t + 1, a.token_blocks)) * kWarps + warp;
     if (unit < static_cast<int64_t>(a.n_tokens) * a.head_chunks) query_warp<kHalf>(a, static_cast<int>(unit), lane);
   }
 }
@@ -251,6 +257,7 @@ cudaError_t launch_norm_rope_append(const NormRopeLaunch& L) {
   a.token_blocks = (a.n_tokens + kWarps - 1) / kWarps;
   const int64_t units = static_cast<int64_t>(a.n_tokens) * a.head_chunks;
   const unsigned blocks = static_cast<unsigned>(a.token_blocks + (units + kWarps - 1) / kWarps);
+  a.period = static_cast<int>(blocks / a.token_blocks);
   MLA_FORMAT_DISPATCH(L, launch_t, L, a, blocks)
   return cudaErrorInvalidValue;
 }
