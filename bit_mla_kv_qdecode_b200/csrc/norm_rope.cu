@@ -16,7 +16,7 @@
 //
 // Bound: bytes. A token reads 1,152 B and writes its 228-388 B slot (and 1,152 B
 // of rows when asked); its queries read and write 128 B a head each. 8,192 tokens
-// of 128 heads (padded): 45.4 us, 5.8 TB/s; with the tokens' blocks ahead of the
+// of 128 heads (padded): 45.4 us, 5.7 TB/s; with the tokens' blocks ahead of the
 // queries' instead of among them 50.6, with 16 heads a warp instead of 32 52.5.
 // A step of 32 tokens is latency, 5.2 us.
 #include "append_token.cuh"
