@@ -97,6 +97,10 @@ def lib_path() -> str:
     return _build.LIB_PATH
 
 
+def binding_path() -> str:
+    return _build.BINDING_PATH
+
+
 def load():
     """Load the built library (building it first only if MLA_BUILD_ON_IMPORT=1)."""
     global _lib

@@ -8,6 +8,8 @@ current CUDA stream to the library. Nothing is computed here.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 
 import torch
 
@@ -15,7 +17,6 @@ from . import _lib
 from ._lib import MlaError, check, make_desc, mla_qcache_desc  # noqa: F401
 
 D_C, D_R, PAGE = 512, 64, 64
-_Tensor, _U8, _I32, _BF16, _F32 = torch.Tensor, torch.uint8, torch.int32, torch.bfloat16, torch.float32
 
 
 def _stream(stream) -> int:
@@ -206,128 +207,29 @@ def mla_qdecode_hybrid(desc, pool, block_table, hist_lens, max_hist_len, bf16_po
     return out, lse
 
 
-def _refuse(t, name, dtype, shape, index):
-    """Raise the error of an argument that does not fit (the contiguity check comes last)."""
-    if not isinstance(t, _Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
-    raise ValueError(f"{name} must be contiguous")
+# The operators around the decode are bound in C++ (csrc/torch_binding.cpp): same checks, a
+# quarter of the host time a call.
+_binding = None
 
 
-def _arg(t, name, dtype, shape, index):
-    """Address of a dense tensor of this type and shape on CUDA device `index`."""
-    if isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index \
-            and t.is_contiguous():
-        return t.data_ptr()
-    _refuse(t, name, dtype, shape, index)
+def _ext():
+    global _binding
+    if _binding is None:
+        _lib.load()
+        path = _lib.binding_path()
+        if not os.path.exists(path):
+            raise ImportError(f"PyTorch binding {path} is missing: build it with "
+                              "`python -m bit_mla_kv_qdecode_b200.build`")
+        spec = importlib.util.spec_from_file_location("_mla_torch", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.set_error(MlaError)
+        _binding = m
+    return _binding
 
 
-def _opt(t, name, dtype, shape, index):
-    return None if t is None else _arg(t, name, dtype, shape, index)
-
-
-def _device_index(t, name, dtype, dims):
-    """CUDA device of the tensor that the other arguments have to join, which has `dims` dimensions."""
-    if not isinstance(t, _Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
-    if not t.is_cuda or t.dtype is not dtype:
-        _refuse(t, name, dtype, t.shape, 0)
-    return t.get_device()
-
-
-def _dense(shape):
-    """Strides of a dense tensor of one to four dimensions."""
-    if len(shape) == 3:
-        return shape[1] * shape[2], shape[2], 1
-    if len(shape) == 2:
-        return shape[1], 1
-    if len(shape) == 1:
-        return (1,)
-    return shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3], 1
-
-
-def _empty(shape, dtype, index, stream):
-    """Uninitialised tensor for a kernel on `stream` (None: the current stream): taken from that
-    stream's memory, and not given back while the current stream may still read it."""
-    if stream is not None:
-        device = torch.device("cuda", index)
-        cur = torch.cuda.current_stream(device)
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device) if int(stream) else torch.cuda.default_stream(device)
-        if stream.cuda_stream != cur.cuda_stream:
-            with torch.cuda.stream(stream):
-                t = torch.empty(shape, dtype=dtype, device=device)
-            t.record_stream(cur)
-            return t
-    return torch.empty_strided(shape, _dense(shape), dtype=dtype, device=index)
-
-
-def _call(name, index, stream, *args):
-    """Run a library call with CUDA device `index` current, on `stream` or that device's current stream."""
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(index)
-    elif isinstance(stream, torch.cuda.Stream):
-        stream = stream.cuda_stream
-    else:
-        stream = int(stream)
-    fn = getattr(_lib.load(), name)
-    if torch.cuda.current_device() == index:
-        code = fn(*args, stream)
-    else:
-        with torch.cuda.device(index):
-            code = fn(*args, stream)
-    if code:
-        check(name, code)
-
-
-def _pool(desc, pool, index):
-    """Address of a quantized pool, which must hold every page of desc."""
-    if not (isinstance(pool, _Tensor) and pool.dtype is _U8 and pool.get_device() == index and pool.is_contiguous()):
-        _refuse(pool, "pool", _U8, getattr(pool, "shape", ()), index)
-    if pool.numel() < desc.num_pages * _lib.load().mla_qcache_page_bytes(ctypes.byref(desc)):
-        raise ValueError("pool is smaller than desc.num_pages pages")
-    return pool.data_ptr()
-
-
-def _table(block_table, B, index):
-    """(address, row length) of a block table of B requests."""
-    if isinstance(block_table, _Tensor):
-        shape = block_table.shape
-        if len(shape) == 2 and shape[0] == B:
-            return _arg(block_table, "block_table", _I32, shape, index), shape[1]
-        raise ValueError(f"block_table must have shape ({B}, max_pages), got {tuple(shape)}")
-    raise TypeError("block_table must be a torch.Tensor")
-
-
-def _rows(t, name, shape, index):
-    """(address, row stride) of a bf16 tensor [B, n, ...] whose B * n rows are evenly spaced."""
-    if not isinstance(t, _Tensor) or t.dtype is not _BF16 or t.shape != shape or t.get_device() != index:
-        _refuse(t, name, _BF16, shape, index)
-    B, n = shape[0], shape[1]
-    stride = t.stride()
-    if t.numel() and (stride[-1] != 1 or (B > 1 and n > 1 and stride[0] != n * stride[1])):
-        raise ValueError(f"{name} must have unit stride in its last dimension and evenly spaced rows")
-    return t.data_ptr(), (stride[1] if n > 1 else stride[0] if B > 1 else 0)
-
-
-def _out_rows(t, name, rows, width, index):
-    """(address, row stride) of a bf16 output [rows, width] with unit stride in a row."""
-    if not isinstance(t, _Tensor) or t.dtype is not _BF16 or t.shape != (rows, width) \
-            or t.get_device() != index:
-        _refuse(t, name, _BF16, (rows, width), index)
-    stride = t.stride()
-    if stride[1] != 1 or (rows > 1 and stride[0] < width):
-        raise ValueError(f"{name} must have unit stride in a row and rows that do not overlap")
-    return t.data_ptr(), stride[0] if rows > 1 else width
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 _ROPE_PAIRS = {"interleaved": _lib.MLA_ROPE_INTERLEAVED, "half": _lib.MLA_ROPE_HALF}
@@ -343,97 +245,32 @@ def mla_qcache_append_norm_rope(desc, pool, block_table, seq_lens_before, kv, no
     pairs = _ROPE_PAIRS.get(convention)
     if pairs is None:
         raise ValueError(f"unknown rotary convention {convention!r}")
-    dev = _device_index(kv, "kv", _BF16, 3)
-    B, n = kv.shape[0], kv.shape[1]
-    pkv, kv_stride = _rows(kv, "kv", (B, n, D_C + D_R), dev)
-    H, pq, q_token, q_head, pqo = 0, None, 0, 0, None
-    if q is not None:
-        if not isinstance(q, _Tensor) or q.dim() != 4:
-            raise ValueError("q must be a tensor [B, n, H, 64]")
-        H = q.shape[2]
-        pq, q_token = _rows(q, "q", (B, n, H, D_R), dev)
-        q_head = q.stride(2) if H > 1 else 0
-        if q_out is None:
-            q_out = _empty((B, n, H, D_R), _BF16, dev, stream)
-        pqo = _arg(q_out, "q_out", _BF16, (B, n, H, D_R), dev)
-        if H == 0:
-            pq = pqo = None
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    if not isinstance(cos_sin, _Tensor) or cos_sin.dim() != 2:
-        raise ValueError(f"cos_sin must be a tensor [positions, {D_R}]")
-    positions_held = cos_sin.shape[0]
-    _call("mla_qcache_append_norm_rope", dev, stream, ctypes.byref(desc), _pool(desc, pool, dev),
-          *_table(block_table, B, dev), _arg(seq_lens_before, "seq_lens_before", _I32, (B,), dev),
-          _opt(new_lens, "new_lens", _I32, (B,), dev), pkv, kv_stride,
-          _opt(norm_weight, "norm_weight", _BF16, (D_C,), dev), float(eps), pq, q_token, q_head, H, pqo,
-          _arg(cos_sin, "cos_sin", _F32, (positions_held, D_R), dev), positions_held,
-          _opt(positions, "positions", _I32, (B, n), dev), pairs,
-          _opt(rows_out, "rows_out", _BF16, (B, n, D_C + D_R), dev), B, n)
-    return q_out
+    return _ext().append_norm_rope(ctypes.addressof(desc), pool, block_table, seq_lens_before, kv, norm_weight, eps, cos_sin,
+                                   pairs, q, q_out, positions, new_lens, rows_out, _handle(stream))
 
 
 def mla_qcache_read(desc, pool, block_table, start, cu_rows, max_rows, out_c=None, out_kr=None, stream=None) -> None:
     """Read dequantized rows back: tokens start[b] + i (start None: 0) of request b into row
     cu_rows[b] + i of out_c [rows, 512] and out_kr [rows, 64] (bf16; either may be None, and both may
     be column ranges of one buffer). max_rows bounds the rows of one request."""
-    out = out_c if out_c is not None else out_kr
-    if not isinstance(out, _Tensor) or out.dim() != 2:
-        raise ValueError("out_c or out_kr must be given, as tensors [rows, width]")
-    dev = _device_index(cu_rows, "cu_rows", _I32, 1)
-    B = cu_rows.shape[0] - 1
-    if B < 0:
-        raise ValueError("cu_rows must have one entry more than there are requests")
-    rows = out.shape[0]
-    pc, sc = (None, 0) if out_c is None else _out_rows(out_c, "out_c", rows, D_C, dev)
-    pr, sr = (None, 0) if out_kr is None else _out_rows(out_kr, "out_kr", rows, D_R, dev)
-    _call("mla_qcache_read", dev, stream, ctypes.byref(desc), _pool(desc, pool, dev), *_table(block_table, B, dev),
-          _opt(start, "start", _I32, (B,), dev), _arg(cu_rows, "cu_rows", _I32, (B + 1,), dev),
-          int(max_rows), rows, pc, sc, pr, sr, B)
+    _ext().qcache_read(ctypes.addressof(desc), pool, block_table, start, cu_rows, max_rows, out_c, out_kr, _handle(stream))
 
 
 def mla_page_digest(desc, pool, block_table, seq_lens_before, n_new, digests, *, new_lens=None, stream=None) -> None:
     """Mean keys of the pages that appending new_lens[b] (None: n_new) tokens completed, into the
     pages' rows of digests [num_pages, 576] (bf16). Call it after the append."""
-    dev = _device_index(seq_lens_before, "seq_lens_before", _I32, 1)
-    B = seq_lens_before.shape[0]
-    _call("mla_page_digest", dev, stream, ctypes.byref(desc), _pool(desc, pool, dev), *_table(block_table, B, dev),
-          _arg(seq_lens_before, "seq_lens_before", _I32, (B,), dev),
-          _opt(new_lens, "new_lens", _I32, (B,), dev), int(n_new),
-          _arg(digests, "digests", _BF16, (desc.num_pages, D_C + D_R), dev), B)
+    _ext().page_digest(ctypes.addressof(desc), pool, block_table, seq_lens_before, n_new, digests, new_lens, _handle(stream))
 
 
 def new_digests(desc: mla_qcache_desc, device="cuda") -> torch.Tensor:
     """Zeroed bf16 digests [num_pages, 576] of a pool's pages."""
-    return torch.zeros((desc.num_pages, D_C + D_R), dtype=_BF16, device=device)
-
-
-def _page_count(max_seq_len) -> int:
-    return max(0, -(-max_seq_len // PAGE))
-
-
-def _queries(q_c, q_r):
-    """(B, s_q, H, device index, addresses of q_c and q_r)."""
-    dev = _device_index(q_c, "q_c", _BF16, 4)
-    B, s_q, H = q_c.shape[:3]
-    return B, s_q, H, dev, _arg(q_c, "q_c", _BF16, (B, s_q, H, D_C), dev), \
-        _arg(q_r, "q_r", _BF16, (B, s_q, H, D_R), dev)
+    return torch.zeros((desc.num_pages, D_C + D_R), dtype=torch.bfloat16, device=device)
 
 
 def mla_page_scores(block_table, seq_lens, max_seq_len, digests, q_c, q_r, scale, *, out=None, stream=None):
     """Expected attention mass of every candidate page, fp32 [B, s_q, ceil(max_seq_len / 64)] (-inf
     for pages that are no candidates). See include/mla_qcache.h."""
-    B, s_q, H, dev, pc, pr = _queries(q_c, q_r)
-    max_seq_len = int(max_seq_len)
-    pages = digests.shape[0] if isinstance(digests, _Tensor) and digests.dim() == 2 else 0
-    pd = _arg(digests, "digests", _BF16, (pages, D_C + D_R), dev)
-    shape = (B, s_q, _page_count(max_seq_len))
-    if out is None:
-        out = _empty(shape, _F32, dev, stream)
-    _call("mla_page_scores", dev, stream, pd, pages, *_table(block_table, B, dev),
-          _arg(seq_lens, "seq_lens", _I32, (B,), dev), max_seq_len, pc, pr, B, s_q, H, float(scale),
-          _arg(out, "out", _F32, shape, dev))
-    return out
+    return _ext().page_scores(block_table, seq_lens, max_seq_len, digests, q_c, q_r, scale, out, _handle(stream))
 
 
 def mla_select_pages(block_table, seq_lens, max_seq_len, scores, k_pages, *, n_sink=1, n_recent=1, s_q=None,
@@ -442,30 +279,8 @@ def mla_select_pages(block_table, seq_lens, max_seq_len, scores, k_pages, *, n_s
     indexes in the request, sel_lens [B, s_q] keys), int32, -1 behind the last page. scores
     [B, s_q, ceil(max_seq_len / 64)] may be None when k_pages covers every page (then s_q is needed).
     sel_table and sel_lens, flattened to B * s_q requests, are what mla_qdecode takes."""
-    if scores is None:
-        if s_q is None:
-            raise ValueError("s_q is needed without scores")
-    elif not isinstance(scores, _Tensor) or scores.dim() != 3:
-        raise ValueError("scores must be a tensor [B, s_q, pages]")
-    else:
-        s_q = scores.shape[1]
-    dev = _device_index(seq_lens, "seq_lens", _I32, 1)
-    B, max_seq_len, k_pages = seq_lens.shape[0], int(max_seq_len), int(k_pages)
-    if k_pages < 1 or s_q < 1:
-        raise MlaError("mla_select_pages", _lib.MLA_ERR_INVALID_ARG)
-    shape = (B, s_q, k_pages)
-    if sel_table is None:
-        sel_table = _empty(shape, _I32, dev, stream)
-    if sel_pages is None:
-        sel_pages = _empty(shape, _I32, dev, stream)
-    if sel_lens is None:
-        sel_lens = _empty((B, s_q), _I32, dev, stream)
-    _call("mla_select_pages", dev, stream, *_table(block_table, B, dev),
-          _arg(seq_lens, "seq_lens", _I32, (B,), dev), max_seq_len,
-          _opt(scores, "scores", _F32, (B, s_q, _page_count(max_seq_len)), dev), B, s_q, k_pages, int(n_sink), int(n_recent),
-          _arg(sel_table, "sel_table", _I32, shape, dev), _arg(sel_pages, "sel_pages", _I32, shape, dev),
-          _arg(sel_lens, "sel_lens", _I32, (B, s_q), dev))
-    return sel_table, sel_pages, sel_lens
+    return _ext().select_pages(block_table, seq_lens, max_seq_len, scores, k_pages, n_sink, n_recent, s_q, sel_table,
+                               sel_pages, sel_lens, _handle(stream))
 
 
 def mla_qdecode_sparse_workspace_bytes(B, s_q, H, max_seq_len, k_pages, num_splits=0) -> int:
@@ -477,25 +292,11 @@ def mla_qdecode_sparse(desc, pool, block_table, seq_lens, max_seq_len, digests, 
                        stream=None):
     """One decode step over the pages that the digests' scores select (scores, selection, decode).
     digests may be None when k_pages covers every page. Returns (out, lse). See include/mla_qcache.h."""
-    B, s_q, H, dev, pc, pr = _queries(q_c, q_r)
-    max_seq_len, k_pages = int(max_seq_len), int(k_pages)
-    if out is None:
-        out = _empty((B, s_q, H, D_C), out_dtype, dev, stream)
-    f32 = out.dtype is _F32
-    if not f32 and out.dtype is not _BF16:
+    if out is None and out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out must be bfloat16 or float32")
-    if workspace is None:
-        with torch.cuda.device(dev):  # the split plan is the device's
-            need = mla_qdecode_sparse_workspace_bytes(B, s_q, H, max_seq_len, k_pages, num_splits)
-        workspace = _empty((max(need, 1),), _U8, dev, stream)
-    nw = workspace.numel()
-    _call("mla_qdecode_sparse", dev, stream, ctypes.byref(desc), _pool(desc, pool, dev), *_table(block_table, B, dev),
-          _arg(seq_lens, "seq_lens", _I32, (B,), dev), max_seq_len,
-          _opt(digests, "digests", _BF16, (desc.num_pages, D_C + D_R), dev), pc, pr, B, s_q, H, float(scale),
-          k_pages, int(n_sink), int(n_recent), int(num_splits), _arg(workspace, "workspace", _U8, (nw,), dev), nw,
-          _arg(out, "out", out.dtype, (B, s_q, H, D_C), dev), f32, _opt(lse, "lse", _F32, (B, s_q, H), dev),
-          int(flags))
-    return out, lse
+    return _ext().qdecode_sparse(ctypes.addressof(desc), pool, block_table, seq_lens, max_seq_len, digests, q_c, q_r, scale,
+                                 k_pages, n_sink, n_recent, out, out_dtype is torch.float32, lse, num_splits, workspace,
+                                 flags, _handle(stream)), lse
 
 
 def mla_cache_bytes_per_request(desc, seq_len, sink=0, window=0) -> int:

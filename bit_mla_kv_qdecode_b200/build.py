@@ -1,7 +1,9 @@
 """Build the CUDA library in-tree: bit_mla_kv_qdecode_b200/lib/libmla_qcache.so.
 
 nvcc compiles every csrc/*.cu for sm_100a only (B200), links them into one
-shared library with a C ABI (include/mla_qcache.h), and needs no GPU.
+shared library with a C ABI (include/mla_qcache.h), and needs no GPU. Where
+PyTorch is installed, its binding of the operators around the decode
+(csrc/torch_binding.cpp) is built beside it and linked against it.
 
     python -m bit_mla_kv_qdecode_b200.build [--verbose]
 """
@@ -12,11 +14,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmla_qcache.so")
+BINDING_PATH = os.path.join(LIB_DIR, "_mla_torch.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -38,6 +42,7 @@ def build(verbose: bool = False, force: bool = False) -> str:
     if not force and os.path.exists(LIB_PATH):
         newest = max(os.path.getmtime(p) for p in deps)
         if os.path.getmtime(LIB_PATH) >= newest:
+            _build_binding(verbose)
             return LIB_PATH
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp = LIB_PATH + ".tmp"
@@ -50,7 +55,35 @@ def build(verbose: bool = False, force: bool = False) -> str:
     if verbose:
         sys.stdout.write(proc.stdout + proc.stderr)
     os.replace(tmp, LIB_PATH)
+    _build_binding(verbose, force)
     return LIB_PATH
+
+
+def _build_binding(verbose: bool = False, force: bool = False) -> None:
+    try:
+        import torch
+    except ImportError:
+        return  # the C ABI and its ctypes binding stand alone
+    src, header = os.path.join(PKG, "csrc", "torch_binding.cpp"), os.path.join(ROOT, "include", "mla_qcache.h")
+    if not force and os.path.exists(BINDING_PATH) and \
+            os.path.getmtime(BINDING_PATH) >= max(os.path.getmtime(src), os.path.getmtime(header)):
+        return
+    where = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    tmp = BINDING_PATH + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", os.path.join(ROOT, "include"), "-I", os.path.join(where, "include"),
+           "-I", os.path.join(where, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), src, "-o", tmp,
+           "-L", LIB_DIR, "-lmla_qcache", "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(where, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError("building the PyTorch binding failed:\n" + proc.stdout + proc.stderr)
+    if verbose:
+        sys.stdout.write(proc.stdout + proc.stderr)
+    os.replace(tmp, BINDING_PATH)
 
 
 if __name__ == "__main__":
