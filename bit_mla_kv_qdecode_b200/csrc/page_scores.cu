@@ -7,7 +7,7 @@
 // Heads are the MMA's M side (one TMEM lane a head), pages its N side, so a
 // head's maximum and sum run along its lane's own columns, with no exchange
 // between lanes; only the last sum, over heads, crosses lanes. A CTA keeps the
-// logits of two tiles in tensor memory: up to 2 * C tiles (131,072 tokens at 8
+// logits of two tiles in tensor memory: up to 2 * C tiles (262,144 tokens at 16
 // CTAs) the statistics of the whole query are known before any logit is read
 // again, and none goes through memory. A longer query's tiles are computed
 // twice, first for the statistics. (Pages as the M side, with the statistics
@@ -49,7 +49,7 @@ namespace {
 
 constexpr int kSoftWarps = 8, kCopyWarps = 4;
 constexpr int kSoftThreads = kSoftWarps * 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kAccs = 3;                           // accumulators of a logit, a warp that issues for each
 constexpr int kMmaWarp = kSoftWarps + kCopyWarps;  // the first of them
 constexpr int kThreads = (kMmaWarp + kAccs) * 32;
@@ -85,8 +85,10 @@ struct Maps {
 struct Misc {
   uint64_t full[kMaxStages], empty[kMaxStages], q_full[kBlocks], t_full[kHeld], t_empty[kHeld], scratch_empty;
   float2 half[kScoreHeads];               // (maximum, sum) of each head over one half of the CTA's pages
-  float2 part[kMaxCluster][kScoreHeads];  // over each CTA's pages, written by the CTAs
-  float mass[2][4][kTile];      // a tile's weights, summed over a quarter of the heads
+  union {
+    float2 part[kMaxCluster][kScoreHeads];  // over each CTA's pages, written by the CTAs
+    float mass[2][4][kTile];                // later: a tile's weights, summed over a quarter of the heads
+  };
   uint32_t ok[2][kTile / 32];   // a tile's pages that count
   uint32_t tmem;
   int abort;
@@ -403,6 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArg
     for (int r = 0; r < C; ++r) sum = fmaf(m.part[r][h].y, exp2_approx(m.part[r][h].x - top), sum);
     if (sum > 0.0f) inv = 1.0f / sum;
   }
+  if (warp < kSoftWarps) soft_sync();  // the parts have been read; the weights take their place
 
   // ---- second sweep: weights and their sum over the heads ----
   if (warp < kSoftWarps) {
@@ -495,9 +498,10 @@ bool make_rows_map(CUtensorMap* m, const void* base, int width, int64_t n, int r
   return encode_swizzled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 2, dims, strides, box);
 }
 
-// Clusters of 1, 2, 4 and 8 CTAs that run at once on the current device (one CTA
-// an SM; clusters stay within a GPC, whose SMs they need not fill). Asked once a device.
-constexpr int kMaxDevices = 64, kSizes = 4;
+// Clusters of 1, 2, 4, 8 and 16 CTAs that run at once on the current device (one
+// CTA an SM; clusters stay within a GPC, whose SMs they need not fill; there may be
+// none of 16). Asked once a device.
+constexpr int kMaxDevices = 64, kSizes = 5;
 static_assert(1 << (kSizes - 1) == kMaxCluster, "cluster sizes");
 std::mutex g_slots_mu;
 int g_slots[kMaxDevices][kSizes];
@@ -512,6 +516,7 @@ cudaError_t cluster_slots(int (&slots)[kSizes]) {
   if (kept[0] == 0) {
     for (auto kern : {page_scores_kernel<false>, page_scores_kernel<true>}) {
       e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return e;
     }
     int got[kSizes];
@@ -526,6 +531,11 @@ cudaError_t cluster_slots(int (&slots)[kSizes]) {
       cfg.attrs = attr;
       cfg.numAttrs = 1;
       e = cudaOccupancyMaxActiveClusters(&got[i], page_scores_kernel<false>, &cfg);
+      if (e != cudaSuccess && i + 1 == kSizes) {
+        cudaGetLastError();  // no GPC takes one
+        got[i] = 0;
+        e = cudaSuccess;
+      }
       if (e != cudaSuccess) return e;
     }
     for (int i = kSizes - 1; i >= 0; --i) kept[i] = std::max(got[i], i == 0 ? 1 : 0);

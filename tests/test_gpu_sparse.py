@@ -75,6 +75,12 @@ def test_scores_lengths(lens, s_q, H):
     _scores_case(lens, s_q, H, seed=len(lens) + H)
 
 
+def test_scores_in_every_cluster_size():
+    """One query to many, short to long: one CTA a query up to sixteen."""
+    for lens in ([64 * 100] * 150, [64 * 200] * 60, [64 * 500] * 30, [64 * 1000] * 12, [64 * 2040 + 1] * 3):
+        _scores_case(lens, 1, 8, seed=len(lens))
+
+
 def test_scores_beyond_one_sweep():
     """More pages than a query's accumulators hold at once."""
     _scores_case([64 * 9000 + 5], 1, 128, seed=2)
