@@ -23,6 +23,24 @@ __device__ __forceinline__ uint32_t quantize_code(float x, float s, float z) {
   return static_cast<uint32_t>(t);
 }
 
+// The same code without a division: the quotient by Markstein's method (P. W. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990), two corrections q += (d - q s) r with r the correctly rounded 1 / s. The
+// first brings q within one unit of its last place, after which the second is the
+// correctly rounded quotient; the remainders are exact for quotients from 1/4 on
+// (s >= 2^-24, an fp16 step), and below that both forms round to code 0. r = 0
+// stands for s = 0. A division an element, each with its own branch for special
+// operands, took 2 of the 5 us of a step's append.
+template <int BITS>
+__device__ __forceinline__ uint32_t quantize_code(float x, float s, float z, float r) {
+  constexpr float qmax = static_cast<float>((1 << BITS) - 1);
+  const float d = __fsub_rn(x, z);
+  float q = __fmul_rn(d, r);
+  q = __fmaf_rn(__fmaf_rn(-q, s, d), r, q);
+  q = __fmaf_rn(__fmaf_rn(-q, s, d), r, q);
+  return static_cast<uint32_t>(fminf(fmaxf(rintf(q), 0.0f), qmax));
+}
+
 // Group scale and zero-point from the group's min and max.
 template <int BITS>
 __device__ __forceinline__ void group_params(float mn, float mx, __half& s16, __half& z16) {
@@ -36,8 +54,9 @@ __device__ __forceinline__ void group_params(float mn, float mx, __half& s16, __
 // RoPE codes, RoPE (s,z). Lane l holds content channels [16l, 16l+16) in x and
 // RoPE channels {2l, 2l+1} in r0, r1 (bf16 values). With kHat, x, r0 and r1 are
 // replaced by the values the written codes stand for, u*s + z (u*s is exact in
-// fp32, so the sum is the one rounding). All 32 lanes call it.
-template <int BITS_C, int G_C, int BITS_R, int G_R, bool kHat>
+// fp32, so the sum is the one rounding). kDivide takes each code by a division (the
+// kernels that have the append inside keep their registers so). All 32 lanes call it.
+template <int BITS_C, int G_C, int BITS_R, int G_R, bool kHat, bool kDivide>
 __device__ __forceinline__ void quantize_values_warp(uint8_t* pg, int slot, float (&x)[16], float& r0, float& r1,
                                                      int lane) {
   using G = QGeom<BITS_C, G_C, BITS_R, G_R>;
@@ -58,10 +77,11 @@ __device__ __forceinline__ void quantize_values_warp(uint8_t* pg, int slot, floa
   __half s16, z16;
   group_params<BITS_C>(mn, mx, s16, z16);
   const float s = __half2float(s16), z = __half2float(z16);
+  const float inv = kDivide || s == 0.0f ? 0.0f : __frcp_rn(s);
   uint32_t packed[2] = {0u, 0u};
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
-    const uint32_t u = quantize_code<BITS_C>(x[k], s, z);
+    const uint32_t u = kDivide ? quantize_code<BITS_C>(x[k], s, z) : quantize_code<BITS_C>(x[k], s, z, inv);
     const int bit = k * BITS_C;
     packed[bit >> 5] |= u << (bit & 31);
     if constexpr (kHat) x[k] = __fmaf_rn(static_cast<float>(u), s, z);
@@ -89,7 +109,9 @@ __device__ __forceinline__ void quantize_values_warp(uint8_t* pg, int slot, floa
   __half rs16, rz16;
   group_params<BITS_R>(rmn, rmx, rs16, rz16);
   const float rs = __half2float(rs16), rz = __half2float(rz16);
-  const uint32_t u0 = quantize_code<BITS_R>(r0, rs, rz), u1 = quantize_code<BITS_R>(r1, rs, rz);
+  const float rinv = kDivide || rs == 0.0f ? 0.0f : __frcp_rn(rs);
+  const uint32_t u0 = kDivide ? quantize_code<BITS_R>(r0, rs, rz) : quantize_code<BITS_R>(r0, rs, rz, rinv);
+  const uint32_t u1 = kDivide ? quantize_code<BITS_R>(r1, rs, rz) : quantize_code<BITS_R>(r1, rs, rz, rinv);
   const uint32_t rbits = u0 | (u1 << BITS_R);
   if constexpr (kHat) {
     r0 = __fmaf_rn(static_cast<float>(u0), rs, rz);
@@ -125,7 +147,7 @@ __device__ __forceinline__ void quantize_token_warp(uint8_t* pg, int slot, const
   }
   const uint32_t rw = __ldg(reinterpret_cast<const uint32_t*>(kr_src) + lane);
   float r0 = bf16_lo(rw), r1 = bf16_hi(rw);
-  quantize_values_warp<BITS_C, G_C, BITS_R, G_R, false>(pg, slot, x, r0, r1, lane);
+  quantize_values_warp<BITS_C, G_C, BITS_R, G_R, false, true>(pg, slot, x, r0, r1, lane);
 }
 
 }  // namespace mla

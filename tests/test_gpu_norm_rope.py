@@ -133,6 +133,28 @@ def test_same_bytes_as_append():
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("fmt", [(4, 64, 4, 64), (2, 32, 2, 32), (4, 32, 2, 64), (2, 64, 4, 32)])
+def test_codes_on_borders(fmt):
+    """The division-free codes against mla_qcache_append's, where quotients meet borders: values that are
+    multiples of half a step, steps from fp16's smallest to large, constant groups. The key part carries
+    them (angle 0 leaves it as it is); the latent is what the norm makes of such values."""
+    rng = np.random.default_rng(sum(fmt))
+    n = 4096
+    step = 2.0 ** rng.integers(-26, 8, (n, 1)) * rng.choice([1.0, 1.5, 1.0625, 1.984375, 0.0], (n, 1), p=[.4, .2, .2, .15, .05])
+    kv = torch.from_numpy((step * rng.integers(-40, 41, (n, 576)) / 2).astype(np.float32)).bfloat16()
+    kv[: n // 2, 512:] += torch.from_numpy((step[: n // 2] * rng.standard_normal((n // 2, 64)) * 4).astype(np.float32)).bfloat16()
+    kv = kv.view(1, n, 576)
+    c = torch.from_numpy(ref.to_bf16_f32(ref.rms_norm(ref.f32(kv)[..., :512], None, EPS))).bfloat16().cuda()
+    desc = api.make_desc(*fmt, num_pages=n // 64)
+    table = torch.arange(n // 64, dtype=torch.int32, device="cuda").view(1, -1)
+    before = torch.zeros(1, dtype=torch.int32, device="cuda")
+    a, b = api.new_qcache_pool(desc), api.new_qcache_pool(desc)
+    api.mla_qcache_append(desc, a, table, before, c, kv[..., 512:].contiguous().cuda())
+    api.mla_qcache_append_norm_rope(desc, b, table, before, kv.cuda(), None, EPS, torch.from_numpy(ref.angle_table(1)).cuda(),
+                                    positions=torch.zeros((1, n), dtype=torch.int32, device="cuda"))
+    assert torch.equal(a, b)
+
+
 def test_bad_slots_and_positions_are_skipped():
     desc = api.make_desc(4, 64, 4, 64, num_pages=2)
     pool = api.new_qcache_pool(desc)
