@@ -23,6 +23,7 @@ using Opt = std::optional<at::Tensor>;
 using Stream = std::optional<int64_t>;  // cudaStream_t; none: the current stream
 
 constexpr int64_t kDc = 512, kDr = 64, kPage = 64;
+constexpr int64_t kMaxSelected = 1 << 20;  // pages a query may attend
 
 PyObject* g_error = nullptr;  // MlaError(function, code), kept for the life of the process
 
@@ -277,7 +278,7 @@ std::tuple<Tensor, Tensor, Tensor> select_pages(const Tensor& table, const Tenso
   const int dev = device_of(seq_lens, "seq_lens", at::kInt, 1);
   const int64_t B = seq_lens.size(0);
   const int max_seq_len = as_int(max_seq_len_, "max_seq_len");
-  if (k < 1 || s_q < 1) check("mla_select_pages", MLA_ERR_INVALID_ARG);
+  if (k < 1 || k > kMaxSelected || s_q < 1 || s_q > 65535) check("mla_select_pages", MLA_ERR_INVALID_ARG);  // before allocating
   const int64_t shape[3] = {B, s_q, k}, score_shape[3] = {B, s_q, page_count(max_seq_len)};
   const auto* ps = arg<float>(scores, "scores", at::kFloat, score_shape, dev);
   const Table tab = table_of(table, B, dev);

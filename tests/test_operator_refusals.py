@@ -188,3 +188,21 @@ def test_binding_refuses_host_tensors_types_and_shapes():
         api.mla_select_pages(table, ints, 100, torch.zeros((1, 2)), 1)
     with pytest.raises(ValueError, match="CUDA"):
         api.mla_qdecode_sparse(desc, pool, table, ints, 100, dig, q_c, q_r, 1.0, 2)
+
+
+def test_binding_refuses_wrong_kinds_of_arguments():
+    desc = api.make_desc(4, 64, 4, 64, num_pages=2)
+    table, ints = torch.zeros((1, 2), dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    dig = torch.zeros((2, 576), dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        api.mla_page_digest(None, dig, table, ints, 1, dig)        # no description
+    with pytest.raises(TypeError):
+        api.mla_page_digest(desc, "pool", table, ints, 1, dig)     # no tensor
+    with pytest.raises(TypeError):
+        api.mla_page_digest(desc, dig, table, ints, 1.5, dig)      # no whole number
+    with pytest.raises(TypeError):
+        api.mla_page_digest(desc, dig, table, ints.long(), 1, dig)
+    with pytest.raises(TypeError):
+        api.mla_qdecode_sparse(desc, dig, table, ints, 100, dig, dig, dig, 1.0, 2, out_dtype=torch.float16)
+    with pytest.raises(ValueError, match="dimensions"):
+        api.mla_page_scores(table, ints, 100, dig, dig, dig, 1.0)
