@@ -4,6 +4,11 @@
 //   rows:    x_hat = bf16(u * s + z)
 //   digest:  kbar_p = bf16( (1/64) sum_t (u_t s_t + z_t) ), fp32 sums
 //
+// Rows are bf16 because the projections that take them are. Digests are bf16 as the
+// scores' operand type and half the bytes to read each step; the rounding, 2^-9 of a
+// channel's mean and independent between channels, is far below what a mean says
+// of its 64 keys.
+//
 // u * s is exact in fp32 (at most 15 significant bits), so u * s + z is one
 // rounding. Codes become floats by setting them into the low bits of 2^23, where
 // they stand in the word, and subtracting it (both at full rate; the conversion
