@@ -14,6 +14,8 @@
 // they stand in the word, and subtracting it (both at full rate; the conversion
 // instruction runs at a quarter of it); the step takes back the power of two
 // that the place is worth. Additions and products are two values an instruction.
+#include <algorithm>
+
 #include "mla_common.cuh"
 #include "mla_internal.h"
 #include "sm100_ptx.cuh"
@@ -442,7 +444,11 @@ cudaError_t launch_read_t(const ReadLaunch& L, const ReadArgs& a) {
   // tokens: 97 us, at two a warp 114); with few CTAs the length of each one's chain
   // counts, and two a warp finish sooner (1,021 tokens: 2.0 us instead of 3.4; even
   // at 32,768 tokens).
-  const unsigned pages = static_cast<unsigned>((static_cast<int64_t>(L.max_rows) + 62) / kPage + 1);
+  // Rows a request can have: no more than the outputs, nor than its table row holds
+  // and one (the first position behind the table row is flagged), however loose
+  // max_rows is. They touch a page more than they fill where they start inside one.
+  const int64_t rows = std::min({static_cast<int64_t>(L.max_rows), L.total_rows, static_cast<int64_t>(L.max_pages) * kPage + 1});
+  const unsigned pages = static_cast<unsigned>((rows + 62) / kPage + 1);
   if (static_cast<int64_t>(pages) * L.B < 4 * 148)
     return launch_dependent(qcache_read_kernel<BC, GC, BR, GR, 2>, dim3(4 * pages, L.B), dim3(kReadThreads), 0, L.stream, a);
   return launch_dependent(qcache_read_kernel<BC, GC, BR, GR, 8>, dim3(pages, L.B), dim3(kReadThreads), 0, L.stream, a);
@@ -450,7 +456,9 @@ cudaError_t launch_read_t(const ReadLaunch& L, const ReadArgs& a) {
 
 template <int BC, int GC, int BR, int GR>
 cudaError_t launch_digest_t(const DigestLaunch& L, const DigestArgs& a) {
-  const int per_request = L.n_new / kPage + 1;
+  // Pages an append can have completed: no more than its table row has and one (the
+  // first behind the row is flagged), however loose n_new is.
+  const int per_request = std::min(L.n_new / kPage, L.max_pages) + 1;
   const int64_t items = static_cast<int64_t>(per_request) * L.B;
   // A CTA a page is as fast up to about a thousand pages, four to an SM twice over (16
   // requests of 64 pages: 7.8 us, the ring 8.1; 32: 16.9 and 14.1; two pages of

@@ -411,7 +411,8 @@ mla_status mla_qcache_append_norm_rope(const mla_qcache_desc* desc, void* pool,
  *   start        device int32 [B] or NULL (0 each).
  *   cu_rows      device int32 [B+1], not decreasing: the first row of each
  *                request, and the end.
- *   max_rows     host upper bound on the rows of one request.
+ *   max_rows     host upper bound on the rows of one request; may be loose (the
+ *                launch is no larger than total_rows and the table allow).
  *   total_rows   rows that the outputs have room for.
  *   out_c        device bf16 [total_rows, 512] with row stride c_stride
  *                (elements), or NULL; out_kr the same, 64 wide, kr_stride. The
