@@ -477,14 +477,10 @@ __global__ void __launch_bounds__(kThreads, 1) page_scores_kernel(const ScoreArg
 
   ptx::tc_fence_before();
   __syncthreads();
+  if (*abort_flag) ptx::linger();  // every thread: none frees tensor memory or leaves before
   if (warp == kMmaWarp) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);
-  }
-  if (tid == 0 && *abort_flag) {  // copies and MMAs in flight get time to end before the memory is given back
-    const uint64_t t0 = ptx::globaltimer_ns();
-    while (ptx::globaltimer_ns() - t0 < 100000ull) {
-    }
   }
 }
 

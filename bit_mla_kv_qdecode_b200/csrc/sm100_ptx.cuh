@@ -20,6 +20,15 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
   return t;
 }
 
+// After a wait that ran out, before the CTA's shared or tensor memory is given
+// back: copies and MMAs still in flight get 100 us to end. Whole warps call it.
+__device__ __forceinline__ void linger() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 100000ull) {
+  }
+  __syncwarp();
+}
+
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));

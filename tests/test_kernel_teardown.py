@@ -1,0 +1,28 @@
+"""Order of a kernel's end after a wait that ran out, read from the source.
+
+The path cannot be run without a broken pipeline, so the order is checked in the text: copies and MMAs
+in flight get their time (`linger`) before tensor memory is freed and before any warp leaves.
+"""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "bit_mla_kv_qdecode_b200", "csrc")
+
+
+def _code(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+@pytest.mark.parametrize("name", ["page_scores.cu"])
+def test_tensor_memory_is_freed_after_the_work_in_flight(name):
+    code = _code(name)
+    free = [m.start() for m in re.finditer(r"ptx::tmem_dealloc\(", code)]
+    assert len(free) == 1
+    # the last barrier of all threads, then the wait of every one of them, then the release
+    barrier = code.rindex("__syncthreads();", 0, free[0])
+    between = code[barrier:free[0]]
+    assert re.search(r"if \(\*abort_flag\) ptx::linger\(\);", between), between
+    assert "globaltimer" not in code[free[0]:code.index("\n}\n", free[0])]
