@@ -419,16 +419,15 @@ __global__ void __launch_bounds__(kDigestThreads + 32, kRingCtas) page_digest_ri
         ptx::mbar_arrive(&m.full[s]);
       }
     }
-    if (!ok) {  // copies in flight get time to land before the memory is given back
-      const uint64_t t0 = ptx::globaltimer_ns();
-      while (ptx::globaltimer_ns() - t0 < 100000ull) {
-      }
-    }
+    if (!ok) ptx::linger();
     return;
   }
   for (int it = 0;; ++it) {
     const int s = it % kRingPages;
-    if (!wait(&m.full[s], (it / kRingPages) & 1)) break;
+    if (!wait(&m.full[s], (it / kRingPages) & 1)) {
+      ptx::linger();  // the copying warp may have left with copies in flight
+      break;
+    }
     const int page = m.page[s];
     if (page < 0) break;
     digest_warp<BC, GC, BR, GR, true>(m.stages[s].content, m.stages[s].rest, a.digests + static_cast<size_t>(page) * kDqk,

@@ -26,3 +26,12 @@ def test_tensor_memory_is_freed_after_the_work_in_flight(name):
     between = code[barrier:free[0]]
     assert re.search(r"if \(\*abort_flag\) ptx::linger\(\);", between), between
     assert "globaltimer" not in code[free[0]:code.index("\n}\n", free[0])]
+
+
+def test_every_leaving_warp_of_the_digest_ring_waits():
+    code = _code("qcache_read.cu")
+    body = code[code.index("page_digest_ring_kernel(const DigestArgs"):]
+    body = body[:body.index("\n}\n")]
+    # both roles: the copying warp and the summing ones
+    assert re.search(r"if \(!ok\) ptx::linger\(\);\s*return;", body)
+    assert re.search(r"if \(!wait\(&m\.full\[s\][^{]*\{\s*ptx::linger\(\);\s*break;", body)
