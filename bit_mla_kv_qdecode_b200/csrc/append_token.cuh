@@ -29,8 +29,10 @@ __device__ __forceinline__ uint32_t quantize_code(float x, float s, float z) {
 // first brings q within one unit of its last place, after which the second is the
 // correctly rounded quotient; the remainders are exact for quotients from 1/4 on
 // (s >= 2^-24, an fp16 step), and below that both forms round to code 0. r = 0
-// stands for s = 0. A division an element, each with its own branch for special
-// operands, took 2 of the 5 us of a step's append.
+// stands for s = 0. z comes from finite_offset: an infinite quotient has no
+// remainder (inf - inf), a very large one ends at the same code. An infinite or NaN
+// step gives code 0 in both forms. A division an element, each with its own branch
+// for special operands, took 2 of the 5 us of a step's append.
 template <int BITS>
 __device__ __forceinline__ uint32_t quantize_code(float x, float s, float z, float r) {
   constexpr float qmax = static_cast<float>((1 << BITS) - 1);
@@ -40,6 +42,10 @@ __device__ __forceinline__ uint32_t quantize_code(float x, float s, float z, flo
   q = __fmaf_rn(__fmaf_rn(-q, s, d), r, q);
   return static_cast<uint32_t>(fminf(fmaxf(rintf(q), 0.0f), qmax));
 }
+
+// Offset for the codes without a division: that of a group whose minimum is below
+// fp16's range is -inf, and every quotient by a finite step the largest code.
+__device__ __forceinline__ float finite_offset(float z) { return fmaxf(z, -1e30f); }
 
 // Group scale and zero-point from the group's min and max.
 template <int BITS>
@@ -77,11 +83,11 @@ __device__ __forceinline__ void quantize_values_warp(uint8_t* pg, int slot, floa
   __half s16, z16;
   group_params<BITS_C>(mn, mx, s16, z16);
   const float s = __half2float(s16), z = __half2float(z16);
-  const float inv = kDivide || s == 0.0f ? 0.0f : __frcp_rn(s);
+  const float inv = kDivide || s == 0.0f ? 0.0f : __frcp_rn(s), zq = finite_offset(z);
   uint32_t packed[2] = {0u, 0u};
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
-    const uint32_t u = kDivide ? quantize_code<BITS_C>(x[k], s, z) : quantize_code<BITS_C>(x[k], s, z, inv);
+    const uint32_t u = kDivide ? quantize_code<BITS_C>(x[k], s, z) : quantize_code<BITS_C>(x[k], s, zq, inv);
     const int bit = k * BITS_C;
     packed[bit >> 5] |= u << (bit & 31);
     if constexpr (kHat) x[k] = __fmaf_rn(static_cast<float>(u), s, z);
@@ -109,9 +115,9 @@ __device__ __forceinline__ void quantize_values_warp(uint8_t* pg, int slot, floa
   __half rs16, rz16;
   group_params<BITS_R>(rmn, rmx, rs16, rz16);
   const float rs = __half2float(rs16), rz = __half2float(rz16);
-  const float rinv = kDivide || rs == 0.0f ? 0.0f : __frcp_rn(rs);
-  const uint32_t u0 = kDivide ? quantize_code<BITS_R>(r0, rs, rz) : quantize_code<BITS_R>(r0, rs, rz, rinv);
-  const uint32_t u1 = kDivide ? quantize_code<BITS_R>(r1, rs, rz) : quantize_code<BITS_R>(r1, rs, rz, rinv);
+  const float rinv = kDivide || rs == 0.0f ? 0.0f : __frcp_rn(rs), rzq = finite_offset(rz);
+  const uint32_t u0 = kDivide ? quantize_code<BITS_R>(r0, rs, rz) : quantize_code<BITS_R>(r0, rs, rzq, rinv);
+  const uint32_t u1 = kDivide ? quantize_code<BITS_R>(r1, rs, rz) : quantize_code<BITS_R>(r1, rs, rzq, rinv);
   const uint32_t rbits = u0 | (u1 << BITS_R);
   if constexpr (kHat) {
     r0 = __fmaf_rn(static_cast<float>(u0), rs, rz);

@@ -187,3 +187,36 @@ def test_empty_calls():
         out = api.mla_qcache_append_norm_rope(desc, pool, table, z, kv, None, EPS, cs, q=kv.new_zeros((B, n, 2, 64)))
         assert out.shape == (B, n, 2, 64)
     assert api.mla_get_device_status() == 0 and int(pool.sum()) == 0
+
+
+@pytest.mark.parametrize("fmt", [(4, 64, 4, 64), (2, 32, 2, 32), (4, 32, 2, 64), (2, 64, 4, 32)])
+def test_same_bytes_as_append_beyond_the_range_of_fp16(fmt):
+    """Offsets that overflow to an infinity, under steps that do and steps that do not: still the bytes of
+    mla_qcache_append, and the oracle's wherever the step is finite. Weights carry the latent out there."""
+    rng = np.random.default_rng(sum(fmt) + 1)
+    n = 256
+    kv = ref.f32(ref.bf16_randn(rng, (1, n, 576)))
+    center = rng.choice([-7e4, -66000.0, -65520.0, -3e5, 7e4, 1e6, 0.0], (n, 1))
+    width = rng.choice([0.0, 600.0, 5e3, 9e4, 3e6], (n, 1))
+    kv[0, :, 512:] = center + width * rng.uniform(-1, 1, (n, 64))
+    kv[0, 0, 512:], kv[0, 1, 512:] = -7e4 + 1000 * (np.arange(64) % 8), -1e38  # a finite step; a step of zero
+    kv = torch.from_numpy(kv).bfloat16()
+    w = torch.from_numpy(np.where(np.arange(512) // 64 % 2, 3e4, 1.0).astype(np.float32)).bfloat16()
+    c = ref.to_bf16_f32(ref.rms_norm(ref.f32(kv)[..., :512], ref.f32(w), EPS))
+    desc = api.make_desc(*fmt, num_pages=n // 64)
+    table = torch.arange(n // 64, dtype=torch.int32, device="cuda").view(1, -1)
+    before = torch.zeros(1, dtype=torch.int32, device="cuda")
+    a, b = api.new_qcache_pool(desc), api.new_qcache_pool(desc)
+    api.mla_qcache_append(desc, a, table, before, torch.from_numpy(c).bfloat16().cuda(), kv[..., 512:].contiguous().cuda())
+    api.mla_qcache_append_norm_rope(desc, b, table, before, kv.cuda(), w.cuda(), EPS, torch.from_numpy(ref.angle_table(1)).cuda(),
+                                    positions=torch.zeros((1, n), dtype=torch.int32, device="cuda"))
+    assert api.mla_get_device_status() == 0
+    assert torch.equal(a, b)
+    d = ref.np_desc(fmt)
+    want = layout.new_pool(d, 1)
+    x = ref.f32(kv)[:, :1, 512:]
+    with np.errstate(over="ignore"):
+        layout.append(d, want, np.zeros((1, 1), int), [0], c[:, :1], x)
+    off = 64 * 512 * fmt[0] // 8  # the key's codes of the first token: every one the largest
+    assert np.all(b[0, off:off + 64 * fmt[2] // 8].cpu().numpy() == 255)
+    assert np.array_equal(b[0, off:off + 64 * fmt[2] // 8].cpu().numpy(), want[0, off:off + 64 * fmt[2] // 8])
