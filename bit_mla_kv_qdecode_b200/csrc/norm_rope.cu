@@ -57,6 +57,13 @@ __device__ __forceinline__ int angle_position(const NormRopeArgs& a, int tok, in
   return p >= 0 && p < a.max_positions ? p : -1;
 }
 
+// Tokens given of request b, or -1 for a count out of range: such a request is
+// skipped, and flagged by the warp of its first token.
+__device__ __forceinline__ int tokens_given(const NormRopeArgs& a, int b) {
+  const int n = a.new_lens ? __ldg(a.new_lens + b) : a.n_new;
+  return n >= 0 && n <= a.n_new ? n : -1;
+}
+
 __device__ __forceinline__ float round_bf16(float v) { return __bfloat162float(__float2bfloat16_rn(v)); }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -77,10 +84,13 @@ __device__ __forceinline__ void token_warp(const NormRopeArgs& a, int tok, int l
   const uint4* ws = reinterpret_cast<const uint4*>(a.weight) + 2 * lane;
   const uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
   const uint4 g0 = a.weight ? __ldg(ws) : ones, g1 = a.weight ? __ldg(ws + 1) : ones;
-  const int given = a.new_lens ? __ldg(a.new_lens + b) : a.n_new;
+  const int given = tokens_given(a, b);
   const int pos = angle_position(a, tok, b, j);
   const int t = __ldg(a.lens_before + b) + j;
-  if (j >= given) return;
+  if (j >= given) {
+    if (given < 0 && j == 0 && lane == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
+    return;
+  }
   const int page = lookup_page(a.table, a.max_pages, a.num_pages, b, t);
   if (pos < 0 || page < 0) {
     if (lane == 0) record_error(a.status, MLA_ERR_INVALID_ARG);
@@ -151,7 +161,7 @@ template <bool kHalf>
 __device__ __forceinline__ void query_warp(const NormRopeArgs& a, int unit, int lane) {
   const int tok = unit / a.head_chunks, chunk = unit - tok * a.head_chunks;
   const int b = tok / a.n_new, j = tok - b * a.n_new;
-  const int given = a.new_lens ? __ldg(a.new_lens + b) : a.n_new;
+  const int given = tokens_given(a, b);
   const int pos = angle_position(a, tok, b, j);
   if (j >= given) return;
   if (pos < 0) {

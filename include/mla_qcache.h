@@ -370,7 +370,8 @@ mla_status mla_qdecode_hybrid(const mla_qcache_desc* desc, const void* pool,
  *                   as for mla_qcache_append.
  *   new_lens        device int32 [B] or NULL: tokens given of request b, in
  *                   [0, n_new]; nothing is written for the padding behind them
- *                   (NULL: n_new each).
+ *                   (NULL: n_new each). A request with a count outside is
+ *                   skipped whole, its queries too, and flagged.
  *   kv              device bf16, row b * n_new + j at kv + row * kv_stride
  *                   elements: 512 latent channels, then 64 of the key (a column
  *                   range of a fused projection's output will do).

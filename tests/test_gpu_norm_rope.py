@@ -220,3 +220,33 @@ def test_same_bytes_as_append_beyond_the_range_of_fp16(fmt):
     off = 64 * 512 * fmt[0] // 8  # the key's codes of the first token: every one the largest
     assert np.all(b[0, off:off + 64 * fmt[2] // 8].cpu().numpy() == 255)
     assert np.array_equal(b[0, off:off + 64 * fmt[2] // 8].cpu().numpy(), want[0, off:off + 64 * fmt[2] // 8])
+
+
+def test_counts_out_of_range_skip_the_request():
+    """new_lens below 0 or above n_new: the append and the digests both leave the request as it is and flag it;
+    the other requests are served."""
+    rng = np.random.default_rng(31)
+    fmt, n, H = (4, 64, 4, 64), 65, 3
+    desc = api.make_desc(*fmt, num_pages=8)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    table, before = i32([[0, 1], [2, 3], [4, 5], [6, 7]]), i32([3, 0, 5, 60])
+    kv, q = ref.bf16_randn(rng, (4, n, 576)).cuda(), ref.bf16_randn(rng, (4, n, H, 64)).cuda()
+    cs = torch.from_numpy(ref.angle_table(200)).cuda()
+
+    def run(new):
+        pool, dig = api.new_qcache_pool(desc), api.new_digests(desc)
+        rows, q_out = torch.full_like(kv, 7.0), torch.full_like(q, 7.0)
+        api.mla_qcache_append_norm_rope(desc, pool, table, before, kv, None, EPS, cs, q=q, q_out=q_out, rows_out=rows,
+                                        new_lens=i32(new))
+        status = api.mla_get_device_status()
+        api.mla_page_digest(desc, pool, table, before, n, dig, new_lens=i32(new))
+        assert api.mla_get_device_status() == status
+        return status, pool, dig, rows, q_out
+
+    ok, *want = run([65, 0, 64, 0])
+    assert ok == 0
+    for a, b in ((66, -1), (-(2 ** 31), 2 ** 31 - 1)):
+        bad, *got = run([65, a, 64, b])
+        assert bad == api._lib.MLA_ERR_INVALID_ARG
+        for x, y in zip(want, got):
+            assert torch.equal(x, y)
