@@ -152,8 +152,8 @@ int page_count(int max_seq_len) { return static_cast<int>((static_cast<long>(max
 
 // Sparse decode workspace: scores, selection (table and lengths), then the
 // scratch of the decode over it, B * s_q requests of one query each. The
-// selection's rows are as wide as a query can need (n_sink + n_recent pages fit
-// there too: a query that sees no more than k_pages takes all of them).
+// selection's rows are no wider than the pages there can be, however large k_pages
+// is.
 struct SparseWorkspace {
   size_t off_scores, off_table, off_lens, off_inner, inner, total;
   int k_pages, max_keys, num_splits;
@@ -190,7 +190,7 @@ SparseWorkspace sparse_workspace(int B, int s_q, int H, int max_seq_len, int k_p
   const size_t queries = static_cast<size_t>(B) * s_q;
   const int width = page_count(max_seq_len);
   SparseWorkspace w{};
-  w.k_pages = k_pages;
+  w.k_pages = std::min(k_pages, std::max(1, width));
   w.max_keys = static_cast<int>(std::min<long>(static_cast<long>(k_pages) * mla::kPage, max_seq_len));
   w.off_scores = 0;
   w.off_table = align_up(k_pages < width ? queries * width * sizeof(float) : 0, 256);
@@ -686,8 +686,9 @@ mla_status mla_qdecode_sparse(const mla_qcache_desc* desc, const void* pool, con
     r = mla_page_scores(digests, desc->num_pages, block_table, max_pages_per_seq, seq_lens, max_seq_len, q_c, q_r, B,
                         s_q, H, scale, scores, stream);
   if (r != MLA_OK) return r;
-  r = mla_select_pages(block_table, max_pages_per_seq, seq_lens, max_seq_len, scores, B, s_q, sw.k_pages, n_sink,
-                       n_recent, sel_table, nullptr, sel_lens, stream);
+  // (a selection of every page names no first and newest ones: they need not fit its rows)
+  r = mla_select_pages(block_table, max_pages_per_seq, seq_lens, max_seq_len, scores, B, s_q, sw.k_pages,
+                       scored ? n_sink : 0, scored ? n_recent : 1, sel_table, nullptr, sel_lens, stream);
   if (r != MLA_OK) return r;
   // B * s_q requests of one query each, over their own tables
   DecodeCommon c{pool, desc->num_pages, sel_table, sw.k_pages, sel_lens, sw.max_keys, q_c, q_r, B * s_q, 1, H, scale,

@@ -439,3 +439,30 @@ def test_batches_of_nothing():
         t, p, n = api.mla_select_pages(table, lens, L, sc, 1, n_sink=0)
         assert bool((t == -1).all()) and bool((p == -1).all()) and bool((n == 0).all())
     assert api.mla_get_device_status() == 0
+
+
+def test_sparse_with_more_pages_asked_for_than_there_are():
+    """The largest k_pages, with first and newest pages beyond the context too, is the dense decode, in a
+    workspace no larger than the pages need."""
+    rng = np.random.default_rng(33)
+    fmt, lens = (4, 64, 4, 64), np.array([300, 64, 1])
+    table, pages = ref.random_table(rng, lens)
+    pool = torch.from_numpy(ref.random_pool(rng, fmt, pages)).cuda()
+    desc = api.make_desc(*fmt, num_pages=pages)
+    for H, k, sink, recent in ((128, 2 ** 20, 1, 1), (16, 2 ** 20, 2 ** 19, 2 ** 19), (20, 6, 3, 3)):
+        q_c, q_r = ref.bf16_randn(rng, (3, 2, H, 512)).cuda(), ref.bf16_randn(rng, (3, 2, H, 64)).cuda()
+        need = api.mla_qdecode_sparse_workspace_bytes(3, 2, H, 300, k, 1)
+        assert need <= 4096
+        ws = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        out, lse = None, torch.empty((3, 2, H), device="cuda")
+        out, _ = api.mla_qdecode_sparse(desc, pool, _i32(table), _i32(lens), 300, None, q_c, q_r, SCALE, k, n_sink=sink,
+                                        n_recent=recent, num_splits=1, lse=lse, workspace=ws[:need])
+        assert api.mla_get_device_status() == 0 and bool((ws[need:] == 0xA5).all())
+        # query i of request b as a request of its own
+        own = _i32([n - 1 + i for n in lens for i in range(2)])
+        rows = _i32(np.repeat(table, 2, 0))
+        lse2 = torch.empty((6, 1, H), device="cuda")
+        want, _ = api.mla_qdecode(desc, pool, rows, own, 300, q_c.view(6, 1, H, 512), q_r.view(6, 1, H, 64), SCALE,
+                                  num_splits=1, lse=lse2)
+        assert api.mla_get_device_status() == 0
+        assert torch.equal(out.view(-1), want.view(-1)) and torch.equal(lse.view(-1), lse2.view(-1))

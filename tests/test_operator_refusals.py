@@ -157,6 +157,16 @@ def test_sparse_workspace(lib):
     assert ws(64, 1, 128, 65536, 200, 1) == ws(64, 1, 128, 65536, 200, 2)
 
 
+def test_sparse_workspace_is_no_wider_than_the_pages(lib):
+    """k_pages above the page count is the way to attend everything; its rows cost no more than the pages."""
+    ws = lib.mla_qdecode_sparse_workspace_bytes
+    for T in (0, 1, 64, 300, 8192):
+        pages = max(1, -(-T // 64))
+        for k in (pages, pages + 1, 1 << 20):
+            assert ws(256, 1, 128, T, k, 1) == ws(256, 1, 128, T, pages, 1), (T, k)
+    assert ws(256, 1, 128, 64, 1 << 20, 1) == 2 * 1024  # a page and a length a query
+
+
 def test_binding_refuses_host_tensors_types_and_shapes():
     desc = api.make_desc(4, 64, 4, 64, num_pages=2)
     pool = torch.zeros((2, 20736), dtype=torch.uint8)
