@@ -161,6 +161,17 @@ void check(const char* function, int code) {
   throw py::error_already_set();
 }
 
+// Refuse, before outputs and workspaces are allocated for it, what the library would
+// refuse after: a selection that cannot be, lengths that the table cannot hold.
+void check_selection(const char* function, int64_t k, int64_t n_sink, int64_t n_recent) {
+  if (k < 1 || k > kMaxSelected || n_sink < 0 || n_recent < 1 || n_sink > k || n_recent > k - n_sink)
+    check(function, MLA_ERR_INVALID_ARG);
+}
+void check_capacity(const char* function, int64_t queries, int max_seq_len, int table_pages) {
+  if (queries > 65535) check(function, MLA_ERR_UNSUPPORTED);
+  if (queries > 0 && max_seq_len > table_pages * kPage) check(function, MLA_ERR_CAPACITY);
+}
+
 Opt append_norm_rope(int64_t desc_, const Tensor& pool, const Tensor& table, const Tensor& before, const Tensor& kv,
                      const Opt& weight, double eps, const Tensor& cos_sin, int pairs, const Opt& q, Opt q_out,
                      const Opt& positions, const Opt& new_lens, const Opt& rows_out, const Stream& stream) {
@@ -258,6 +269,7 @@ Tensor page_scores(const Tensor& table, const Tensor& seq_lens, int64_t max_seq_
   const void* pd = arg(digests, "digests", at::kBFloat16, {pages, kDc + kDr}, q.dev);
   const Table tab = table_of(table, q.B, q.dev);
   const auto* pl = arg<int32_t>(seq_lens, "seq_lens", at::kInt, {q.B}, q.dev);
+  check_capacity("mla_page_scores", q.B * q.s_q, max_seq_len, tab.pages);
   const int64_t shape[3] = {q.B, q.s_q, page_count(max_seq_len)};
   const Tensor out = out_ ? *out_ : empty(shape, at::kFloat, q.dev, stream);
   auto* po = arg<float>(out, "out", at::kFloat, shape, q.dev);
@@ -278,11 +290,13 @@ std::tuple<Tensor, Tensor, Tensor> select_pages(const Tensor& table, const Tenso
   const int dev = device_of(seq_lens, "seq_lens", at::kInt, 1);
   const int64_t B = seq_lens.size(0);
   const int max_seq_len = as_int(max_seq_len_, "max_seq_len");
-  if (k < 1 || k > kMaxSelected || s_q < 1 || s_q > 65535) check("mla_select_pages", MLA_ERR_INVALID_ARG);  // before allocating
+  check_selection("mla_select_pages", k, n_sink, n_recent);
+  if (s_q < 1 || s_q > 65535) check("mla_select_pages", MLA_ERR_INVALID_ARG);
   const int64_t shape[3] = {B, s_q, k}, score_shape[3] = {B, s_q, page_count(max_seq_len)};
   const auto* ps = arg<float>(scores, "scores", at::kFloat, score_shape, dev);
   const Table tab = table_of(table, B, dev);
   const auto* pl = arg<int32_t>(seq_lens, "seq_lens", at::kInt, {B}, dev);
+  check_capacity("mla_select_pages", B * s_q, max_seq_len, tab.pages);
   const Tensor t = sel_table_ ? *sel_table_ : empty(shape, at::kInt, dev, stream);
   const Tensor p = sel_pages_ ? *sel_pages_ : empty(shape, at::kInt, dev, stream);
   const Tensor l = sel_lens_ ? *sel_lens_ : empty({B, s_q}, at::kInt, dev, stream);
@@ -305,12 +319,14 @@ Tensor qdecode_sparse(int64_t desc_, const Tensor& pool, const Tensor& table, co
   const Queries q = queries(q_c, q_r);
   const int max_seq_len = as_int(max_seq_len_, "max_seq_len"), B = as_int(q.B, "q_c"), s_q = as_int(q.s_q, "q_c"),
             H = as_int(q.H, "q_c"), k_pages = as_int(k, "k_pages"), splits = as_int(num_splits, "num_splits");
+  const Table tab = table_of(table, q.B, q.dev);
+  check_selection("mla_qdecode_sparse", k, n_sink, n_recent);
+  check_capacity("mla_qdecode_sparse", q.B * q.s_q, max_seq_len, tab.pages);
   const int64_t shape[4] = {q.B, q.s_q, q.H, kDc};
   const Tensor out = out_ ? *out_ : empty(shape, f32 ? at::kFloat : at::kBFloat16, q.dev, stream);
   f32 = out.scalar_type() == at::kFloat;
   if (!f32 && out.scalar_type() != at::kBFloat16) throw py::type_error("out must be bfloat16 or float32");
   void* po = arg(out, "out", out.scalar_type(), shape, q.dev);
-  const Table tab = table_of(table, q.B, q.dev);
   const void* pp = pool_of(desc, pool, q.dev);
   const auto* pl = arg<int32_t>(seq_lens, "seq_lens", at::kInt, {q.B}, q.dev);
   const void* pd = arg(digests, "digests", at::kBFloat16, {desc->num_pages, kDc + kDr}, q.dev);

@@ -466,3 +466,35 @@ def test_sparse_with_more_pages_asked_for_than_there_are():
                                   num_splits=1, lse=lse2)
         assert api.mla_get_device_status() == 0
         assert torch.equal(out.view(-1), want.view(-1)) and torch.equal(lse.view(-1), lse2.view(-1))
+
+
+def test_impossible_calls_are_refused_before_anything_is_allocated():
+    B, H, k = 64, 2, 2 ** 20
+    desc = api.make_desc(4, 64, 4, 64, num_pages=2)
+    pool, dig = api.new_qcache_pool(desc), api.new_digests(desc)
+    table, lens = torch.zeros((B, 2), dtype=torch.int32, device="cuda"), torch.ones(B, dtype=torch.int32, device="cuda")
+    q_c = torch.zeros((B, 1, H, 512), dtype=torch.bfloat16, device="cuda")
+    q_r = torch.zeros((B, 1, H, 64), dtype=torch.bfloat16, device="cuda")
+    inv, cap, uns = api._lib.MLA_ERR_INVALID_ARG, api._lib.MLA_ERR_CAPACITY, api._lib.MLA_ERR_UNSUPPORTED
+    bad = [(k, dict(n_sink=-1), 128, inv), (k, dict(n_recent=0), 128, inv), (k, dict(n_sink=k), 128, inv), (0, {}, 128, inv),
+           (k + 1, {}, 128, inv), (k, dict(n_sink=2 ** 40), 128, inv), (k, dict(n_recent=2 ** 62, n_sink=2 ** 62), 128, inv),
+           (k, {}, 129, cap), (2, {}, 2 ** 31 - 1, cap)]
+    torch.cuda.synchronize()
+    held = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    for pages, kw, L, code in bad:
+        with pytest.raises(api.MlaError) as e:
+            api.mla_select_pages(table, lens, L, None, pages, s_q=1, **kw)
+        assert e.value.code == code
+        with pytest.raises(api.MlaError) as e:
+            api.mla_qdecode_sparse(desc, pool, table, lens, L, dig, q_c, q_r, SCALE, pages, **kw)
+        assert e.value.code == code
+    with pytest.raises(api.MlaError) as e:
+        api.mla_select_pages(table, lens, 128, None, k, s_q=1024)
+    assert e.value.code == uns
+    with pytest.raises(api.MlaError) as e:
+        api.mla_page_scores(table, lens, 2 ** 31 - 1, dig, q_c, q_r, SCALE)
+    assert e.value.code == cap
+    assert torch.cuda.max_memory_allocated() == held
+    api.mla_select_pages(table, lens, 128, None, 2, s_q=1)
+    assert api.mla_get_device_status() == 0
