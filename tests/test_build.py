@@ -1,0 +1,35 @@
+"""Building where PyTorch's binding cannot be built, or is another PyTorch's (CPU; no compiler runs)."""
+import subprocess
+
+import pytest
+
+from bit_mla_kv_qdecode_b200 import _lib
+from bit_mla_kv_qdecode_b200 import build as _build
+
+
+@pytest.fixture
+def built():
+    _build.build()
+
+
+@pytest.mark.parametrize("failure", ["no compiler", "no headers", "no toolkit"])
+def test_the_library_stands_without_its_binding(built, monkeypatch, tmp_path, failure):
+    binding = tmp_path / "_mla_torch.so"
+    binding.write_bytes(b"of older sources")
+    monkeypatch.setattr(_build, "BINDING_PATH", str(binding))
+    monkeypatch.setattr(_build.os.path, "getmtime", lambda p, real=_build.os.path.getmtime: 0.0 if p == str(binding) else real(p))
+
+    def run(cmd, **kw):
+        if failure == "no compiler":
+            raise FileNotFoundError(2, "No such file or directory", cmd[0])
+        return subprocess.CompletedProcess(cmd, 1, "", "fatal error: cuda_runtime_api.h: No such file or directory")
+
+    monkeypatch.setattr(_build.subprocess, "run", run)
+    if failure == "no toolkit":
+        def none():
+            raise RuntimeError("nvcc not found")
+        monkeypatch.setattr(_build, "nvcc_path", none)
+    with pytest.warns(UserWarning, match="binding"):
+        assert _build.build() == _build.LIB_PATH
+    assert not binding.exists()  # not taken for a binding of this library
+    assert _lib.load().mla_qcache_layout_version() == 1
