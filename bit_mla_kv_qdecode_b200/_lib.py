@@ -98,7 +98,7 @@ def lib_path() -> str:
 
 
 def binding_path() -> str:
-    return _build.BINDING_PATH
+    return _build.binding_path()
 
 
 def load():

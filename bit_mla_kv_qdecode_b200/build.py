@@ -21,8 +21,14 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmla_qcache.so")
-BINDING_PATH = os.path.join(LIB_DIR, "_mla_torch.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
+
+
+def binding_path() -> str:
+    """Where the binding for the installed PyTorch is: its name carries the versions whose binary interface it is
+    compiled for, so that another PyTorch's or Python's is not taken for it."""
+    import torch
+    return os.path.join(LIB_DIR, f"_mla_torch-{torch.__version__}-{sys.implementation.cache_tag}.so")
 
 
 def nvcc_path() -> str:
@@ -68,11 +74,11 @@ def _build_binding(verbose: bool = False, force: bool = False) -> None:
     except ImportError:
         return  # the C ABI and its ctypes binding stand alone
     src, header = os.path.join(PKG, "csrc", "torch_binding.cpp"), os.path.join(ROOT, "include", "mla_qcache.h")
-    if not force and os.path.exists(BINDING_PATH) and \
-            os.path.getmtime(BINDING_PATH) >= max(os.path.getmtime(src), os.path.getmtime(header)):
+    path = binding_path()
+    if not force and os.path.exists(path) and os.path.getmtime(path) >= max(os.path.getmtime(src), os.path.getmtime(header)):
         return
     where = os.path.dirname(torch.__file__)
-    tmp = BINDING_PATH + ".tmp"
+    tmp = path + ".tmp"
     try:
         cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
         cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
@@ -87,13 +93,13 @@ def _build_binding(verbose: bool = False, force: bool = False) -> None:
     except (OSError, RuntimeError) as e:
         why = str(e)
     if why is not None:
-        if os.path.exists(BINDING_PATH):
-            os.remove(BINDING_PATH)  # of older sources
+        if os.path.exists(path):
+            os.remove(path)  # of older sources
         warnings.warn(f"{LIB_PATH} is built, its PyTorch binding is not; api's operators around the decode need it:\n{why}")
         return
     if verbose:
         sys.stdout.write(proc.stdout + proc.stderr)
-    os.replace(tmp, BINDING_PATH)
+    os.replace(tmp, path)
 
 
 if __name__ == "__main__":

@@ -16,7 +16,7 @@ def built():
 def test_the_library_stands_without_its_binding(built, monkeypatch, tmp_path, failure):
     binding = tmp_path / "_mla_torch.so"
     binding.write_bytes(b"of older sources")
-    monkeypatch.setattr(_build, "BINDING_PATH", str(binding))
+    monkeypatch.setattr(_build, "binding_path", lambda: str(binding))
     monkeypatch.setattr(_build.os.path, "getmtime", lambda p, real=_build.os.path.getmtime: 0.0 if p == str(binding) else real(p))
 
     def run(cmd, **kw):
@@ -33,3 +33,23 @@ def test_the_library_stands_without_its_binding(built, monkeypatch, tmp_path, fa
         assert _build.build() == _build.LIB_PATH
     assert not binding.exists()  # not taken for a binding of this library
     assert _lib.load().mla_qcache_layout_version() == 1
+
+
+def test_another_pytorch_has_another_binding(built, monkeypatch):
+    import torch
+    mine, ran = _lib.binding_path(), []
+    assert _build.os.path.exists(mine)
+
+    def run(cmd, **kw):
+        ran.append(cmd[cmd.index("-o") + 1])
+        return subprocess.CompletedProcess(cmd, 1, "", "not run")
+
+    monkeypatch.setattr(_build.subprocess, "run", run)
+    _build.build()
+    assert ran == []  # up to date
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    assert _lib.binding_path() != mine and not _build.os.path.exists(_lib.binding_path())
+    with pytest.warns(UserWarning, match="binding"):
+        _build.build()
+    assert len(ran) == 1 and ran[0].startswith(_lib.binding_path())
+    assert _build.os.path.exists(mine)
