@@ -101,6 +101,10 @@ def binding_path() -> str:
     return _build.binding_path()
 
 
+def build_binding() -> None:
+    _build.build_binding()
+
+
 def load():
     """Load the built library (building it first only if MLA_BUILD_ON_IMPORT=1)."""
     global _lib

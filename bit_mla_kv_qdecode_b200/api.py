@@ -217,6 +217,8 @@ def _ext():
     if _binding is None:
         _lib.load()
         path = _lib.binding_path()
+        if not os.path.exists(path) and os.environ.get("MLA_BUILD_ON_IMPORT") == "1":
+            _lib.build_binding()
         if not os.path.exists(path):
             raise ImportError(f"PyTorch binding {path} is missing: build it with "
                               "`python -m bit_mla_kv_qdecode_b200.build`")

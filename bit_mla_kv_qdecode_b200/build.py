@@ -49,7 +49,7 @@ def build(verbose: bool = False, force: bool = False) -> str:
     if not force and os.path.exists(LIB_PATH):
         newest = max(os.path.getmtime(p) for p in deps)
         if os.path.getmtime(LIB_PATH) >= newest:
-            _build_binding(verbose)
+            build_binding(verbose)
             return LIB_PATH
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp = LIB_PATH + ".tmp"
@@ -62,11 +62,11 @@ def build(verbose: bool = False, force: bool = False) -> str:
     if verbose:
         sys.stdout.write(proc.stdout + proc.stderr)
     os.replace(tmp, LIB_PATH)
-    _build_binding(verbose, force)
+    build_binding(verbose, force)
     return LIB_PATH
 
 
-def _build_binding(verbose: bool = False, force: bool = False) -> None:
+def build_binding(verbose: bool = False, force: bool = False) -> None:
     """The binding, where PyTorch is installed. The library stands without it: where it cannot be built (no C++
     compiler, no CUDA headers, a PyTorch without CUDA), that is a warning here and an ImportError at its first use."""
     try:
