@@ -585,8 +585,8 @@ mla_status mla_qcache_read(const mla_qcache_desc* desc, const void* pool, const 
   int* status = status_ptr();
   if (!status) return MLA_ERR_CUDA;
   mla::ReadLaunch L{pool, desc->num_pages, block_table, max_pages_per_seq, start, cu_rows, max_rows, total_rows, out_c,
-                    c_stride, out_kr, kr_stride, B, desc->bits_c, desc->group_c, desc->bits_r, desc->group_r, status,
-                    reinterpret_cast<cudaStream_t>(stream)};
+                    c_stride, out_kr, kr_stride, B, desc->bits_c, desc->group_c, desc->bits_r, desc->group_r,
+                    device_sm_count(), status, reinterpret_cast<cudaStream_t>(stream)};
   return from_cuda(mla::launch_qcache_read(L));
 }
 
@@ -604,7 +604,7 @@ mla_status mla_page_digest(const mla_qcache_desc* desc, const void* pool, const 
   int* status = status_ptr();
   if (!status) return MLA_ERR_CUDA;
   mla::DigestLaunch L{pool, desc->num_pages, block_table, max_pages_per_seq, seq_lens_before, new_lens, n_new, digests,
-                      B, desc->bits_c, desc->group_c, desc->bits_r, desc->group_r, status,
+                      B, desc->bits_c, desc->group_c, desc->bits_r, desc->group_r, device_sm_count(), status,
                       reinterpret_cast<cudaStream_t>(stream)};
   return from_cuda(mla::launch_page_digest(L));
 }

@@ -112,6 +112,7 @@ struct ReadLaunch {
   int64_t kr_stride;
   int B;
   int bits_c, group_c, bits_r, group_r;
+  int sms;  // of the device
   int* status;
   cudaStream_t stream;
 };
@@ -129,6 +130,7 @@ struct DigestLaunch {
   void* digests;
   int B;
   int bits_c, group_c, bits_r, group_r;
+  int sms;  // of the device
   int* status;
   cudaStream_t stream;
 };

@@ -439,16 +439,16 @@ __global__ void __launch_bounds__(kDigestThreads + 32, kRingCtas) page_digest_ri
 
 template <int BC, int GC, int BR, int GR>
 cudaError_t launch_read_t(const ReadLaunch& L, const ReadArgs& a) {
-  // Eight tokens a warp keep four in flight for longer (64 requests of up to 16,384
-  // tokens: 97 us, at two a warp 114); with few CTAs the length of each one's chain
-  // counts, and two a warp finish sooner (1,021 tokens: 2.0 us instead of 3.4; even
-  // at 32,768 tokens).
   // Rows a request can have: no more than the outputs, nor than its table row holds
   // and one (the first position behind the table row is flagged), however loose
   // max_rows is. They touch a page more than they fill where they start inside one.
   const int64_t rows = std::min({static_cast<int64_t>(L.max_rows), L.total_rows, static_cast<int64_t>(L.max_pages) * kPage + 1});
   const unsigned pages = static_cast<unsigned>((rows + 62) / kPage + 1);
-  if (static_cast<int64_t>(pages) * L.B < 4 * 148)
+  // Eight tokens a warp keep four in flight for longer (64 requests of up to 16,384
+  // tokens: 97 us, at two a warp 114); with few CTAs the length of each one's chain
+  // counts, and two a warp finish sooner (1,021 tokens: 2.0 us instead of 3.4; even
+  // at 32,768 tokens).
+  if (static_cast<int64_t>(pages) * L.B < 4 * L.sms)
     return launch_dependent(qcache_read_kernel<BC, GC, BR, GR, 2>, dim3(4 * pages, L.B), dim3(kReadThreads), 0, L.stream, a);
   return launch_dependent(qcache_read_kernel<BC, GC, BR, GR, 8>, dim3(pages, L.B), dim3(kReadThreads), 0, L.stream, a);
 }
@@ -462,15 +462,12 @@ cudaError_t launch_digest_t(const DigestLaunch& L, const DigestArgs& a) {
   // A CTA a page is as fast up to about a thousand pages, four to an SM twice over (16
   // requests of 64 pages: 7.8 us, the ring 8.1; 32: 16.9 and 14.1; two pages of
   // 128 requests: 2.5 and 3.0).
-  if (items < 8 * 148 || items > 0x7fffffff || L.num_pages < 1)
+  if (items < 8 * L.sms || items > 0x7fffffff || L.num_pages < 1)
     return launch_dependent(page_digest_kernel<BC, GC, BR, GR>, dim3(per_request, L.B), dim3(kDigestThreads), 0, L.stream, a);
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   auto kern = page_digest_ring_kernel<BC, GC, BR, GR>;
   constexpr int kSmem = sizeof(RingOf<BC, GC, BR, GR>) + 1024;
   static_assert(kRingCtas * (kSmem + 1024) <= 233472, "CTAs an SM");
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   using G = QGeom<BC, GC, BR, GR>;
   CUtensorMap codes;
@@ -478,7 +475,7 @@ cudaError_t launch_digest_t(const DigestLaunch& L, const DigestArgs& a) {
   const cuuint32_t box[3] = {128, kPage, 1};
   if (!encode_swizzled(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<const uint8_t*>(L.pool) + G::kOffCC, 3, dims, strides, box))
     return cudaErrorInvalidValue;
-  return launch_dependent(kern, dim3(kRingCtas * sms), dim3(kDigestThreads + 32), kSmem, L.stream, a, codes, per_request,
+  return launch_dependent(kern, dim3(kRingCtas * L.sms), dim3(kDigestThreads + 32), kSmem, L.stream, a, codes, per_request,
                           static_cast<int>(items));
 }
 

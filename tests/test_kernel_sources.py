@@ -1,7 +1,8 @@
-"""Order of a kernel's end after a wait that ran out, read from the source.
+"""What no run can show, read from the kernels' sources.
 
-The path cannot be run without a broken pipeline, so the order is checked in the text: copies and MMAs
-in flight get their time (`linger`) before tensor memory is freed and before any warp leaves.
+The end of a kernel after a wait that ran out needs a broken pipeline to run, so its order is checked in
+the text: copies and MMAs in flight get their time (`linger`) before tensor memory is freed and before
+any warp leaves. Launch rules go by the device's own SM count, which one machine cannot vary.
 """
 import os
 import re
@@ -35,3 +36,8 @@ def test_every_leaving_warp_of_the_digest_ring_waits():
     # both roles: the copying warp and the summing ones
     assert re.search(r"if \(!ok\) ptx::linger\(\);\s*return;", body)
     assert re.search(r"if \(!wait\(&m\.full\[s\][^{]*\{\s*ptx::linger\(\);\s*break;", body)
+
+
+@pytest.mark.parametrize("name", ["page_scores.cu", "page_select.cu", "qcache_read.cu", "norm_rope.cu"])
+def test_launch_rules_name_no_sm_count(name):
+    assert not re.search(r"\b14[48]\b", _code(name))
