@@ -12,6 +12,12 @@ fuses into existing parameters:
   cache stores c'. The down-projection absorbs T (W_DKV' = T W_DKV) and every
   consumer of c absorbs T^-1 (W_UK' = W_UK T^-1, W_UV' = W_UV T^-1), so keys,
   values and scores are unchanged.
+  Models that norm the latent (c = w * norm(x), x = W_DKV h, norm the RMS norm)
+  need another split, since a norm does not commute with D, nor R with w: the
+  weights of the norm go into the consumers, T acts on norm(x), R goes into the
+  down-projection (norm(R x) = R norm(x), R being orthogonal) and D takes the
+  place of the norm's weights: D norm(R W_DKV h) = T norm(x). That is what
+  mla_qcache_append_norm_rope takes: kv from R W_DKV, norm_weight = D.
 * RoPE path: M acts inside each rotary pair as a 2-D rotation and one shared
   scale, M = (+)_i s_i R(phi_i). Such an M commutes with RoPE (2-D rotations
   commute; the scale is uniform in the pair), so it folds into the key
@@ -94,6 +100,23 @@ def fold_content(W_dkv: np.ndarray, W_uk: np.ndarray, W_uv: np.ndarray, T: np.nd
     W_uv [H, d_v, d_c] up-project it per head."""
     Tinv = np.linalg.inv(np.asarray(T, dtype=np.float64))
     return T @ W_dkv, np.asarray(W_uk, dtype=np.float64) @ Tinv, np.asarray(W_uv, dtype=np.float64) @ Tinv
+
+
+def fold_normed_content(W_dkv: np.ndarray, W_uk: np.ndarray, W_uv: np.ndarray, norm_weight, rotation: np.ndarray,
+                        scale: np.ndarray):
+    """Fold the content transform T = diag(scale) @ rotation of a latent that is normed between the down-projection
+    and the cache: returns (W_dkv', norm weights, W_uk', W_uv') = (R W_dkv, scale, W_uk diag(w) T^-1, W_uv diag(w) T^-1).
+
+    norm_weight [d_c] is the model's (None: ones); T acts on the normed latent without it. The norm weights returned
+    replace it; mla_qcache_append_norm_rope takes them in bf16, so pass a scale of bf16 values: the up-projections
+    then take back exactly what the cache was given."""
+    content_transform(rotation, scale)  # checks
+    rotation, scale = np.asarray(rotation, dtype=np.float64), np.asarray(scale, dtype=np.float64)
+    w = np.ones(scale.size) if norm_weight is None else np.asarray(norm_weight, dtype=np.float64)
+    if w.shape != scale.shape:
+        raise ValueError("one norm weight per channel")
+    back = w[:, None] * rotation.T / scale  # diag(w) T^-1
+    return rotation @ W_dkv, scale, np.asarray(W_uk, dtype=np.float64) @ back, np.asarray(W_uv, dtype=np.float64) @ back
 
 
 def fold_rope(W_kr: np.ndarray, W_qr: np.ndarray, M: np.ndarray):

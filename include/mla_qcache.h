@@ -19,6 +19,9 @@
  * The learned transforms of the method are folded into the model weights
  * offline, so none run here; q_c arrives already multiplied by W_UK^T and the
  * output o is consumed by W_UV outside the library.
+ * (mla_qcache_append_norm_rope, which norms the latent on its way into the cache,
+ * takes the content transform's channel scales in the place of the norm's weights;
+ * see there.)
  *
  * Quantizer (per token, per group of channels, asymmetric round-to-nearest):
  *     s = fp16(fp32(max - min) / (2^bits - 1)),  z = fp16(min),
@@ -376,6 +379,12 @@ mla_status mla_qdecode_hybrid(const mla_qcache_desc* desc, const void* pool,
  *                   elements: 512 latent channels, then 64 of the key (a column
  *                   range of a fused projection's output will do).
  *   norm_weight     device bf16 [512], or NULL (w = 1).
+ *                   With a content transform T = D R (D scales channels, R is
+ *                   orthogonal) these are D's scales: the latent comes from
+ *                   R W_DKV, the model's own norm weights go into W_UK and W_UV
+ *                   together with T^-1, and the cache holds T norm(W_DKV h). The
+ *                   fold for latents that are not normed, T W_DKV, is wrong here:
+ *                   D does not commute with the norm.
  *   eps             > 0, finite (as the fp32 value passed).
  *   q               device bf16, head h of row r at
  *                   q + r * q_token_stride + h * q_head_stride, 64 channels; NULL
