@@ -1,7 +1,8 @@
 """GPU tests of the launch sizes under loose host bounds: max_rows and n_new may be any int, the work
 launched for them is what the outputs and the block table allow.
 
-The calls are captured into a graph and their grids read from its nodes, before anything runs.
+The calls are captured into a graph and their grids read from its nodes, before anything runs. The scores'
+grids show which cluster sizes their tests reach.
 """
 import ctypes
 
@@ -109,3 +110,16 @@ def test_digest_flags_the_page_behind_the_table():
         api.mla_page_digest(desc, pool, table, _i32([0]), ANY, out, new_lens=_i32([new]))
         assert api.mla_get_device_status() == api._lib.MLA_ERR_INVALID_ARG
         assert torch.equal(out, good)
+
+
+def test_scores_reach_every_cluster_size():
+    """The shapes of the scores' cluster-size test take one CTA a query up to sixteen, a size each."""
+    got = []
+    for tokens, B in ((64 * 100, 150), (64 * 200, 60), (64 * 500, 30), (64 * 1000, 12), (64 * 2040 + 1, 3)):
+        pages = -(-tokens // 64)
+        table, lens = torch.zeros((B, pages), dtype=torch.int32, device="cuda"), _i32(np.full(B, tokens))
+        dig = torch.zeros((1, 576), dtype=torch.bfloat16, device="cuda")
+        q_c, q_r = (torch.zeros((B, 1, 8, d), dtype=torch.bfloat16, device="cuda") for d in (512, 64))
+        (ctas,) = _grids(lambda: api.mla_page_scores(table, lens, tokens, dig, q_c, q_r, 0.1))
+        got.append(ctas / B)
+    assert got == [1, 2, 4, 8, 16]
