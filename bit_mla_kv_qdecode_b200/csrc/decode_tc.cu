@@ -960,7 +960,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // ---- teardown ----
   ptx::tc_fence_before();
   __syncthreads();
-  if (*abort_flag) ptx::linger();  // MMAs in flight end before their tensor memory is another CTA's
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);

@@ -17,7 +17,7 @@ def _code(name):
         return re.sub(r"//[^\n]*", "", f.read())
 
 
-@pytest.mark.parametrize("name", ["page_scores.cu", "decode_tc.cu"])
+@pytest.mark.parametrize("name", ["page_scores.cu"])
 def test_tensor_memory_is_freed_after_the_work_in_flight(name):
     code = _code(name)
     free = [m.start() for m in re.finditer(r"ptx::tmem_dealloc\(", code)]
@@ -26,6 +26,7 @@ def test_tensor_memory_is_freed_after_the_work_in_flight(name):
     barrier = code.rindex("__syncthreads();", 0, free[0])
     between = code[barrier:free[0]]
     assert re.search(r"if \(\*abort_flag\) ptx::linger\(\);", between), between
+    assert "globaltimer" not in code[free[0]:code.index("\n}\n", free[0])]
 
 
 def test_every_leaving_warp_of_the_digest_ring_waits():
