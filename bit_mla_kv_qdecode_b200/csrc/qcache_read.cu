@@ -5,7 +5,7 @@
 //   digest:  kbar_p = bf16( (1/64) sum_t (u_t s_t + z_t) ), fp32 sums
 //
 // Rows are bf16 because the projections that take them are. Digests are bf16 as the
-// scores' operand type and half the bytes to read each step; the rounding, 2^-9 of a
+// scores' operand type and half the bytes to read each step; the rounding, at most 2^-8 of a
 // channel's mean and independent between channels, is far below what a mean says
 // of its 64 keys.
 //
@@ -341,8 +341,12 @@ __global__ void __launch_bounds__(kDigestThreads) page_digest_kernel(const Diges
 // there. The content codes come as TMA boxes in the 128-byte swizzle: a warp's
 // fragment takes 32 bytes from each of four tokens, whose rows would otherwise
 // share their banks (or, read from global memory directly, take four lines a load).
-// Bound: instructions (2,048 pages: 14.1 us; the copies alone 8.6, the sums alone
-// about 12; bytes, 14,592-24,832 read and 1,152 written a page, 6.8).
+// Bound: latency. 2,048 pages take 14.7 us, 1,810 of them 14.1 (pools in turn, so that
+// none stays in L2), where bytes (14,592-24,832 read and 1,152 written a page) would take
+// 6.8 and 6.0; with the profiler's counters issue slots are 29 % busy, the tensor pipe
+// 31 %, memory at a third of its rate, and warps wait for their operands: each loads its
+// page's words, then multiplies, and two CTAs an SM are 27 % of the warps. The copies alone
+// take 8.6 us, the sums alone about 12.
 constexpr int kRingPages = 4, kRingCtas = 2;
 constexpr uint64_t kRingWaitNs = 2000000000ull;
 
@@ -459,9 +463,9 @@ cudaError_t launch_digest_t(const DigestLaunch& L, const DigestArgs& a) {
   // first behind the row is flagged), however loose n_new is.
   const int per_request = std::min(L.n_new / kPage, L.max_pages) + 1;
   const int64_t items = static_cast<int64_t>(per_request) * L.B;
-  // A CTA a page is as fast up to about a thousand pages, four to an SM twice over (16
-  // requests of 64 pages: 7.8 us, the ring 8.1; 32: 16.9 and 14.1; two pages of
-  // 128 requests: 2.5 and 3.0).
+  // A CTA a page is as fast up to about a thousand pages, four to an SM twice over (pools
+  // in L2: 16 requests of 64 pages 7.8 us, the ring 8.1; 32: 16.9 and 14.1; two pages
+  // of 128 requests: 2.5 and 3.0).
   if (items < 8 * L.sms || items > 0x7fffffff || L.num_pages < 1)
     return launch_dependent(page_digest_kernel<BC, GC, BR, GR>, dim3(per_request, L.B), dim3(kDigestThreads), 0, L.stream, a);
   auto kern = page_digest_ring_kernel<BC, GC, BR, GR>;
